@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "mx.cuh"
 #include "trace.h"
 
 using namespace lcvq;
@@ -110,6 +111,15 @@ BwdWs bwd_ws(int64_t M, int64_t d_out, int64_t d_in, int d) {
   return w;
 }
 
+// backward from a kept X: the plain backward's scratch, then the values of X
+size_t bwd_ckpt_values_off(int64_t M, int64_t d_out, int64_t d_in, int d) {
+  return round_up(bwd_ws(M, d_out, d_in, d).total, 256);
+}
+size_t bwd_ckpt_ws(lcvq_dtype dtype, int64_t M, int64_t d_out, int64_t d_in, int d) {
+  return round_up(bwd_ckpt_values_off(M, d_out, d_in, d) +
+                      size_t(M) * size_t(d_in) * (dtype == LCVQ_BF16 ? 2 : 4), 256);
+}
+
 lcvq_status finish(cudaError_t e, int launches) {
   if (e != cudaSuccess) return LCVQ_ERR_CUDA;
   g_last_launches = launches;
@@ -180,6 +190,9 @@ size_t lcvq_workspace_size(lcvq_op op, lcvq_dtype dtype, int64_t M, int64_t d_ou
   if (op == LCVQ_OP_FIT_AFFINE) return kWsHeaderBytes + fit_partials_bytes(d_out, d_in, d);
   if (op == LCVQ_OP_ASSIGN_LDLQ) return kWsHeaderBytes + ldlq_workspace_bytes(d_out, d_in);
   if (op == LCVQ_OP_FIT_AFFINE_H) return kWsHeaderBytes + fith_scratch_bytes(d_out, d_in, d);
+  if (op == LCVQ_OP_MX4_GEMM) return kWsHeaderBytes;
+  if (op == LCVQ_OP_GEMM_CKPT) return gemm_ws(dtype, M, d_in).total;
+  if (op == LCVQ_OP_GEMM_BACKWARD_CKPT) return bwd_ckpt_ws(dtype, M, d_out, d_in, d);
   return 0;
 }
 
@@ -506,6 +519,146 @@ lcvq_status lcvq_gemm_backward(const void* X, const void* dY, lcvq_dtype dtype, 
   }
   if (e == cudaSuccess) e = launch_reduce_partials(partials, parts, d, dA, dB, s, &launches);
   return finish(e, launches);
+}
+
+size_t lcvq_mx_scale_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > kMaxGemmDim || cols % mx::kBlock != 0) return 0;
+  return size_t(mx::scale_bytes(rows, cols));
+}
+
+static lcvq_status validate_mx(int64_t rows, int64_t cols, lcvq_mx_format fmt, lcvq_dtype dtype) {
+  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > kMaxGemmDim || cols % mx::kBlock != 0)
+    return LCVQ_ERR_INVALID_ARG;
+  if (rows * ceil_div(cols, 256) >= (int64_t(1) << 34)) return LCVQ_ERR_INVALID_ARG;  // the grid
+  if (fmt != LCVQ_MX4 && fmt != LCVQ_MX8) return LCVQ_ERR_INVALID_ARG;
+  if (dtype != LCVQ_F32 && dtype != LCVQ_BF16) return LCVQ_ERR_INVALID_ARG;
+  return LCVQ_OK;
+}
+
+lcvq_status lcvq_mx_pack(const void* X, lcvq_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                         lcvq_mx_format fmt, uint8_t* q, uint8_t* scales, void* stream) {
+  LCVQ_API_RANGE();
+  g_last_launches = 0;
+  if (lcvq_status st = validate_mx(rows, cols, fmt, dtype); st != LCVQ_OK) return st;
+  if (ld < cols || ld > (int64_t(1) << 40)) return LCVQ_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return LCVQ_OK;
+  if (!X || !q || !scales) return LCVQ_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(q) || !aligned16(scales) || ld % (dtype == LCVQ_BF16 ? 8 : 4) != 0)
+    return LCVQ_ERR_ALIGNMENT;
+  if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
+  int launches = 0;
+  cudaError_t e = launch_mx_pack(X, dtype == LCVQ_F32, rows, cols, ld, fmt == LCVQ_MX4, q, scales,
+                                 static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+lcvq_status lcvq_mx_decode(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
+                           lcvq_mx_format fmt, void* out, lcvq_dtype dtype, void* stream) {
+  LCVQ_API_RANGE();
+  g_last_launches = 0;
+  if (lcvq_status st = validate_mx(rows, cols, fmt, dtype); st != LCVQ_OK) return st;
+  if (rows == 0 || cols == 0) return LCVQ_OK;
+  if (!q || !scales || !out) return LCVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(scales) || !aligned16(out)) return LCVQ_ERR_ALIGNMENT;
+  if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
+  int launches = 0;
+  cudaError_t e = launch_mx_decode(q, scales, rows, cols, fmt == LCVQ_MX4, out, dtype == LCVQ_F32,
+                                   static_cast<cudaStream_t>(stream), &launches);
+  return finish(e, launches);
+}
+
+lcvq_status lcvq_mx4_gemm(const uint8_t* X4, const uint8_t* SX, int64_t M, const uint8_t* W4,
+                          const uint8_t* SW, int64_t d_out, int64_t d_in, void* Y,
+                          lcvq_dtype y_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  LCVQ_API_RANGE();
+  g_last_launches = 0;
+  if (lcvq_status st = validate_gemm_shapes(y_dtype, M, d_out, d_in, 8); st != LCVQ_OK) return st;
+  if (M == 0 || d_out == 0) return LCVQ_OK;
+  if (!Y) return LCVQ_ERR_INVALID_ARG;
+  if (!aligned16(Y)) return LCVQ_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f32 = y_dtype == LCVQ_F32;
+  if (d_in == 0) {
+    if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
+    if (cudaMemsetAsync(Y, 0, size_t(M) * size_t(d_out) * (f32 ? 4 : 2), s) != cudaSuccess)
+      return LCVQ_ERR_CUDA;
+    return LCVQ_OK;
+  }
+  if (!X4 || !SX || !W4 || !SW || !workspace) return LCVQ_ERR_INVALID_ARG;
+  if (!aligned16(X4) || !aligned16(SX) || !aligned16(W4) || !aligned16(SW) || !aligned16(workspace))
+    return LCVQ_ERR_ALIGNMENT;
+  if (ws_bytes < lcvq_workspace_size(LCVQ_OP_MX4_GEMM, y_dtype, M, d_out, d_in, 8))
+    return LCVQ_ERR_WORKSPACE;
+  if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
+  int launches = 0;
+  cudaError_t e = launch_mx4_gemv(X4, SX, M, W4, SW, d_out, d_in, Y, f32, s, &launches);
+  return finish(e, launches);
+}
+
+lcvq_status lcvq_gemm_ckpt(const void* X, lcvq_dtype dtype, int64_t M, const uint8_t* packed,
+                           int64_t d_out, int64_t d_in, int d, const float* A, const float* B,
+                           void* Y, uint8_t* X8, uint8_t* S8, void* workspace, size_t ws_bytes,
+                           void* stream) {
+  LCVQ_API_RANGE();
+  g_last_launches = 0;
+  if (lcvq_status st = validate_gemm_shapes(dtype, M, d_out, d_in, d); st != LCVQ_OK) return st;
+  const bool keep = M > 0 && d_in > 0;
+  if (keep) {
+    if (lcvq_status st = validate_mx(M, d_in, LCVQ_MX8, dtype); st != LCVQ_OK) return st;
+    if (!X || !X8 || !S8) return LCVQ_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(X8) || !aligned16(S8)) return LCVQ_ERR_ALIGNMENT;
+    if (d_out > 0) {  // everything lcvq_gemm would refuse, before the first launch
+      if (!Y || !packed || !A || !B || !workspace) return LCVQ_ERR_INVALID_ARG;
+      if (!aligned16(Y) || !aligned16(packed) || !aligned16(A) || !aligned16(B) || !aligned16(workspace))
+        return LCVQ_ERR_ALIGNMENT;
+      if (ws_bytes < gemm_ws(dtype, M, d_in).total) return LCVQ_ERR_WORKSPACE;
+    }
+    if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
+  }
+  int launches = 0;
+  if (keep) {
+    cudaError_t e = launch_mx_pack(X, dtype == LCVQ_F32, M, d_in, d_in, false, X8, S8,
+                                   static_cast<cudaStream_t>(stream), &launches);
+    if (e != cudaSuccess) return LCVQ_ERR_CUDA;
+  }
+  lcvq_status st = lcvq_gemm(X, dtype, M, packed, d_out, d_in, d, A, B, Y, LCVQ_FORM_AUTO, workspace,
+                             ws_bytes, stream);
+  if (st != LCVQ_OK) return st;
+  g_last_launches += launches;
+  return LCVQ_OK;
+}
+
+lcvq_status lcvq_gemm_backward_ckpt(const uint8_t* X8, const uint8_t* S8, const void* dY,
+                                    lcvq_dtype dtype, int64_t M, const uint8_t* packed,
+                                    const uint8_t* mask_bits, int64_t d_out, int64_t d_in, int d,
+                                    const float* A, const float* B, void* dX, float* dA, float* dB,
+                                    float* dWp, void* workspace, size_t ws_bytes, void* stream) {
+  LCVQ_API_RANGE();
+  g_last_launches = 0;
+  if (lcvq_status st = validate_gemm_shapes(dtype, M, d_out, d_in, d); st != LCVQ_OK) return st;
+  if (M == 0 || d_out == 0 || d_in == 0)  // empty sums: X is not read
+    return lcvq_gemm_backward(nullptr, dY, dtype, M, packed, mask_bits, d_out, d_in, d, A, B, dX, dA,
+                              dB, dWp, workspace, ws_bytes, stream);
+  if (lcvq_status st = validate_mx(M, d_in, LCVQ_MX8, dtype); st != LCVQ_OK) return st;
+  if (!dA || !dB || (dWp && !mask_bits)) return LCVQ_ERR_INVALID_ARG;
+  if (!X8 || !S8 || !dY || !packed || !A || !B || !workspace) return LCVQ_ERR_INVALID_ARG;
+  if (!aligned16(dA) || !aligned16(dB) || (dWp && !aligned16(dWp)) || (dX && !aligned16(dX)) ||
+      (mask_bits && !aligned16(mask_bits)) || !aligned16(X8) || !aligned16(S8) || !aligned16(dY) ||
+      !aligned16(packed) || !aligned16(A) || !aligned16(B) || !aligned16(workspace))
+    return LCVQ_ERR_ALIGNMENT;
+  if (ws_bytes < bwd_ckpt_ws(dtype, M, d_out, d_in, d)) return LCVQ_ERR_WORKSPACE;
+  if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
+  const size_t off = bwd_ckpt_values_off(M, d_out, d_in, d);
+  void* X = static_cast<char*>(workspace) + off;
+  int launches = 0;
+  cudaError_t e = launch_mx_decode(X8, S8, M, d_in, false, X, dtype == LCVQ_F32,
+                                   static_cast<cudaStream_t>(stream), &launches);
+  if (e != cudaSuccess) return LCVQ_ERR_CUDA;
+  lcvq_status st = lcvq_gemm_backward(X, dY, dtype, M, packed, mask_bits, d_out, d_in, d, A, B, dX,
+                                      dA, dB, dWp, workspace, off, stream);
+  if (st != LCVQ_OK) return st;
+  g_last_launches += launches;
+  return LCVQ_OK;
 }
 
 lcvq_status lcvq_check_device_error(void* workspace, void* stream) {

@@ -129,6 +129,17 @@ cudaError_t launch_ldlq(const float* P, const float* U, int64_t d_out, int64_t d
                         uint8_t* packed, float* E, unsigned int* err, cudaStream_t s,
                         int* launches);
 
+// ---- block-scaled formats (mx.cuh) ----
+cudaError_t launch_mx_pack(const void* X, bool f32, int64_t rows, int64_t cols, int64_t ld, bool mx4,
+                           uint8_t* q, uint8_t* scales, cudaStream_t s, int* launches);
+cudaError_t launch_mx_decode(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
+                             bool mx4, void* out, bool f32, cudaStream_t s, int* launches);
+// Y = X W^T of two mx4 matrices on the integer MMA, tiles of 16 rows of W and
+// up to 32 tokens
+cudaError_t launch_mx4_gemv(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
+                            const uint8_t* ws, int64_t N, int64_t K, void* Y, bool f32,
+                            cudaStream_t s, int* launches);
+
 // ---- tcgen05 GEMMs (bf16, persistent, one CTA per SM) ----
 int tc_max_grid();
 // Xa is X'' (algebraic, with corr) or X (decode form, A z + B decoded on chip)

@@ -6,7 +6,7 @@ raises on a non-OK status.  There is no fallback: if ``liblcvq.so`` is missing
 or fails to load, every call raises.
 
 Names follow the C ABI (``include/lcvq.h``): assign_pack, decode, gemm,
-gemm_backward, workspace_size, check_device_error.
+gemm_backward, workspace_size, check_device_error, mx_pack, mx4_gemm, gemm_ckpt, ...
 """
 
 from __future__ import annotations
@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblcvq.so"
 F32, BF16 = 0, 1
 FORMS = {"auto": 0, "decode": 1, "algebraic": 2}
 OP_GEMM, OP_GEMM_BACKWARD, OP_FIT_AFFINE, OP_ASSIGN_LDLQ, OP_FIT_AFFINE_H = 0, 1, 2, 3, 4
+OP_MX4_GEMM, OP_GEMM_CKPT, OP_GEMM_BACKWARD_CKPT = 5, 6, 7
+MX_FORMATS = {"mx4": 0, "mx8": 1}
 STATUS = {
     0: "LCVQ_OK",
     1: "LCVQ_ERR_INVALID_ARG",
@@ -43,6 +45,12 @@ EXPORTS = (
     "lcvq_fit_affine_h",
     "lcvq_dge_scale",
     "lcvq_assign_ldlq",
+    "lcvq_mx_pack",
+    "lcvq_mx_decode",
+    "lcvq_mx_scale_bytes",
+    "lcvq_mx4_gemm",
+    "lcvq_gemm_ckpt",
+    "lcvq_gemm_backward_ckpt",
     "lcvq_workspace_size",
     "lcvq_workspace_size_grouped",
     "lcvq_check_device_error",
@@ -92,6 +100,15 @@ def lib() -> ctypes.CDLL:
         L.lcvq_fit_affine_h.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
         L.lcvq_dge_scale.argtypes = [_vp, _vp, _i64, ctypes.c_float, _vp]
         L.lcvq_assign_ldlq.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _sz, _vp]
+        L.lcvq_mx_pack.argtypes = [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]
+        L.lcvq_mx_decode.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _i32, _vp]
+        L.lcvq_mx_scale_bytes.argtypes = [_i64, _i64]
+        L.lcvq_mx_scale_bytes.restype = _sz
+        L.lcvq_mx4_gemm.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i32, _vp, _sz, _vp]
+        L.lcvq_gemm_ckpt.argtypes = [_vp, _i32, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _sz, _vp]
+        L.lcvq_gemm_backward_ckpt.argtypes = [_vp, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _i64, _i32,
+                                              _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
         L.lcvq_workspace_size.argtypes = [_i32, _i32, _i64, _i64, _i64, _i32]
         L.lcvq_workspace_size.restype = _sz
         L.lcvq_check_device_error.argtypes = [_vp, _vp]
@@ -101,7 +118,8 @@ def lib() -> ctypes.CDLL:
         for fn in ("lcvq_assign_pack", "lcvq_decode", "lcvq_gemm", "lcvq_gemm_backward",
                    "lcvq_xform", "lcvq_gemm_xformed", "lcvq_gemv_static", "lcvq_gemm_grouped",
                    "lcvq_fit_affine", "lcvq_fit_affine_h", "lcvq_dge_scale", "lcvq_assign_ldlq",
-                   "lcvq_check_device_error",
+                   "lcvq_mx_pack", "lcvq_mx_decode", "lcvq_mx4_gemm", "lcvq_gemm_ckpt",
+                   "lcvq_gemm_backward_ckpt", "lcvq_check_device_error",
                    "lcvq_last_launch_count"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L
@@ -363,3 +381,180 @@ def dge_scale(dWp: torch.Tensor, Wp: torch.Tensor, k: float, *, stream=None) -> 
     _check("lcvq_dge_scale", lib().lcvq_dge_scale(_ptr(dWp), _ptr(Wp), dWp.numel(), float(k),
                                                   _stream(stream)))
     return dWp
+
+
+# ---- block-scaled formats (lcvq_mx_format in include/lcvq.h) ----
+# These calls take byte buffers whose meaning depends on shapes, so the binding
+# checks types, shapes and contiguity, and makes the tensors' device current.
+
+def _need(t, name: str, dtype, shape, dev):
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"lcvq: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _ws(t, dev):
+    if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"lcvq: the workspace must be a contiguous uint8 tensor on {dev}, got {t.dtype} "
+                         f"on {t.device}")
+    return t.data_ptr(), t.numel()
+
+
+def _mx_rows(t, name: str):
+    if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"lcvq: {name} must be a 2-D float32 or bfloat16 tensor, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"lcvq: expected a CUDA tensor, got one on {t.device}")
+
+
+def _on_device(fn, name: str, dev, args, stream):
+    """fn(*args, stream) with dev current (the C ABI works on the current device)."""
+    if dev.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream() if stream is None else stream
+        return _check(name, fn(*args, s.cuda_stream))
+    with torch.cuda.device(dev):
+        s = torch.cuda.current_stream() if stream is None else stream
+        return _check(name, fn(*args, s.cuda_stream))
+
+
+def mx_scale_bytes(rows: int, cols: int) -> int:
+    """Bytes of the scales of a [rows][cols] matrix in a block-scaled format."""
+    return int(lib().lcvq_mx_scale_bytes(rows, cols))
+
+
+def mx_pack(X: torch.Tensor, fmt: str, *, q=None, scales=None, stream=None):
+    """X [rows][cols] (fp32 or bf16, rows contiguous but possibly strided) packed
+    into "mx4" or "mx8": (q, scales), see lcvq_mx_pack."""
+    _mx_rows(X, "X")
+    rows, cols = X.shape
+    f, dev = MX_FORMATS[fmt], X.device
+    if cols % 32:
+        raise ValueError(f"lcvq: a block-scaled row has a multiple of 32 columns, got {cols}")
+    if cols and X.stride(1) != 1:
+        raise ValueError("lcvq: the rows of X must be contiguous")
+    ld = X.stride(0) if rows > 1 else cols
+    qs, nb = (rows, cols // 2 if f == 0 else cols), -(-rows // 128) * -(-cols // 128) * 512
+    q = torch.empty(qs, dtype=torch.uint8, device=dev) if q is None else _need(q, "q", torch.uint8, qs, dev)
+    if scales is None:
+        scales = torch.empty(nb, dtype=torch.uint8, device=dev)
+    else:
+        _need(scales, "scales", torch.uint8, (nb,), dev)
+    _on_device(lib().lcvq_mx_pack, "lcvq_mx_pack", dev,
+               (X.data_ptr(), _dtype_code(X.dtype), rows, cols, ld, f, q.data_ptr(), scales.data_ptr()),
+               stream)
+    return q, scales
+
+
+def mx_decode(q: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str, *, dtype=torch.bfloat16,
+              out=None, stream=None) -> torch.Tensor:
+    """The values [rows][cols] that (q, scales) stand for, exactly."""
+    if not q.is_cuda:
+        raise ValueError(f"lcvq: expected a CUDA tensor, got one on {q.device}")
+    f, dev, rows = MX_FORMATS[fmt], q.device, q.shape[0]
+    _need(q, "q", torch.uint8, (rows, cols // 2 if f == 0 else cols), dev)
+    _need(scales, "scales", torch.uint8, (-(-rows // 128) * -(-cols // 128) * 512,), dev)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+    else:
+        _need(out, "out", out.dtype, (rows, cols), dev)
+    _on_device(lib().lcvq_mx_decode, "lcvq_mx_decode", dev,
+               (q.data_ptr(), scales.data_ptr(), rows, cols, f, out.data_ptr(), _dtype_code(out.dtype)),
+               stream)
+    return out
+
+
+def mx4_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, *,
+             dtype=torch.bfloat16, workspace=None, out=None, stream=None) -> torch.Tensor:
+    """Y = X W^T of two "mx4" matrices (see lcvq_mx4_gemm): (xq, xs) the tokens,
+    (wq, ws) the weights [d_out][d_in].  Y [M][d_out] in dtype."""
+    if not xq.is_cuda:
+        raise ValueError(f"lcvq: expected a CUDA tensor, got one on {xq.device}")
+    dev, (M, kb), N = xq.device, xq.shape, wq.shape[0]
+    kt = -(-kb // 64)
+    _need(xq, "xq", torch.uint8, (M, kb), dev)
+    _need(wq, "wq", torch.uint8, (N, kb), dev)
+    _need(xs, "xs", torch.uint8, (-(-M // 128) * kt * 512,), dev)
+    _need(ws, "ws", torch.uint8, (-(-N // 128) * kt * 512,), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=dev)
+    else:
+        _need(out, "out", out.dtype, (M, N), dev)
+    if workspace is None:
+        workspace = new_workspace(workspace_size(OP_MX4_GEMM, out.dtype, M, N, 2 * kb, 8), dev)
+    _on_device(lib().lcvq_mx4_gemm, "lcvq_mx4_gemm", dev,
+               (xq.data_ptr(), xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, 2 * kb,
+                out.data_ptr(), _dtype_code(out.dtype), *_ws(workspace, dev)), stream)
+    return out
+
+
+def _layer(packed, d_in, A, B, d, dev):
+    d_out = packed.shape[0]
+    _need(packed, "packed", torch.uint8, (d_out, d_in // 4), dev)
+    _need(A, "A", torch.float32, (d, d), dev)
+    _need(B, "B", torch.float32, (d,), dev)
+    return d_out
+
+
+def gemm_ckpt(X: torch.Tensor, packed: torch.Tensor, d_in: int, A: torch.Tensor, B: torch.Tensor,
+              d: int, *, workspace=None, out=None, kept=None, stream=None):
+    """Forward of a training step that keeps X in 8 bits: (Y, kept) with Y = X W~
+    as gemm computes it and kept = mx_pack(X, "mx8") for gemm_backward_ckpt."""
+    _mx_rows(X, "X")
+    dev, M = X.device, X.shape[0]
+    _need(X, "X", X.dtype, (M, d_in), dev)
+    d_out = _layer(packed, d_in, A, B, d, dev)
+    nb = -(-M // 128) * -(-d_in // 128) * 512
+    if kept is None:
+        kept = (torch.empty((M, d_in), dtype=torch.uint8, device=dev),
+                torch.empty(nb, dtype=torch.uint8, device=dev))
+    else:
+        _need(kept[0], "kept[0]", torch.uint8, (M, d_in), dev)
+        _need(kept[1], "kept[1]", torch.uint8, (nb,), dev)
+    if out is None:
+        out = torch.empty((M, d_out), dtype=X.dtype, device=dev)
+    else:
+        _need(out, "out", X.dtype, (M, d_out), dev)
+    if workspace is None:
+        workspace = new_workspace(workspace_size(OP_GEMM_CKPT, X.dtype, M, d_out, d_in, d), dev)
+    _on_device(lib().lcvq_gemm_ckpt, "lcvq_gemm_ckpt", dev,
+               (X.data_ptr(), _dtype_code(X.dtype), M, packed.data_ptr(), d_out, d_in, d, A.data_ptr(),
+                B.data_ptr(), out.data_ptr(), kept[0].data_ptr(), kept[1].data_ptr(),
+                *_ws(workspace, dev)), stream)
+    return out, kept
+
+
+def gemm_backward_ckpt(kept, dY: torch.Tensor, packed: torch.Tensor, mask, d_in: int,
+                       A: torch.Tensor, B: torch.Tensor, d: int, *, want_dx: bool = True,
+                       want_dwp: bool = True, workspace=None, outs=None, stream=None) -> dict:
+    """gemm_backward with X as gemm_ckpt kept it: dict(dX, dA, dB, dWp) (dX / dWp
+    None when not wanted; mask may be None then)."""
+    _mx_rows(dY, "dY")
+    dev, M = dY.device, dY.shape[0]
+    d_out = _layer(packed, d_in, A, B, d, dev)
+    _need(dY, "dY", dY.dtype, (M, d_out), dev)
+    _need(kept[0], "kept[0]", torch.uint8, (M, d_in), dev)
+    _need(kept[1], "kept[1]", torch.uint8, (-(-M // 128) * -(-d_in // 128) * 512,), dev)
+    if mask is not None:
+        _need(mask, "mask", torch.uint8, (d_out, d_in // 8), dev)
+    o = dict(outs or {})
+    want = {"dX": ((M, d_in), dY.dtype, want_dx), "dWp": ((d_out, d_in), torch.float32, want_dwp),
+            "dA": ((d, d), torch.float32, True), "dB": ((d,), torch.float32, True)}
+    for k, (shape, dtype, wanted) in want.items():
+        if not wanted:
+            o[k] = None
+        elif o.get(k) is None:
+            o[k] = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _need(o[k], k, dtype, shape, dev)
+    if workspace is None:
+        workspace = new_workspace(
+            workspace_size(OP_GEMM_BACKWARD_CKPT, dY.dtype, M, d_out, d_in, d), dev)
+    ptr = {k: None if o[k] is None else o[k].data_ptr() for k in want}
+    _on_device(lib().lcvq_gemm_backward_ckpt, "lcvq_gemm_backward_ckpt", dev,
+               (kept[0].data_ptr(), kept[1].data_ptr(), dY.data_ptr(), _dtype_code(dY.dtype), M,
+                packed.data_ptr(), None if mask is None else mask.data_ptr(), d_out, d_in, d,
+                A.data_ptr(), B.data_ptr(), ptr["dX"], ptr["dA"], ptr["dB"], ptr["dWp"],
+                *_ws(workspace, dev)), stream)
+    return o

@@ -112,8 +112,33 @@ typedef enum {
   LCVQ_OP_GEMM_BACKWARD = 1,
   LCVQ_OP_FIT_AFFINE = 2,
   LCVQ_OP_ASSIGN_LDLQ = 3,
-  LCVQ_OP_FIT_AFFINE_H = 4
+  LCVQ_OP_FIT_AFFINE_H = 4,
+  LCVQ_OP_MX4_GEMM = 5,
+  LCVQ_OP_GEMM_CKPT = 6,
+  LCVQ_OP_GEMM_BACKWARD_CKPT = 7
 } lcvq_op;
+
+/* Block-scaled formats.  A block is 32 consecutive elements of a row; its scale
+ * is the smallest power of two s >= 2^-127 with max |x| <= top s, its elements
+ * are x / s rounded to the format's grid (to nearest, ties to even) and stand
+ * for element * s:
+ *   MX4  top = 6, grid 0, 0.5, 1, 1.5, 2, 3, 4, 6 and the negatives (e2m1);
+ *        [rows][cols/2] bytes, byte i holding element 2i in its low nibble and
+ *        element 2i + 1 in its high one (bit 3 of a nibble is the sign).
+ *   MX8  top = 127, the integers -127 .. 127; [rows][cols] bytes, bit 7 the
+ *        sign, bits 0..6 the magnitude; in each group of four elements the
+ *        bytes hold elements 0, 2, 1, 3.
+ * No element is clipped: each is within half a step of its block's grid (where
+ * rounding up would give a value of 2^128 the element below is taken).  A block
+ * with a NaN or an infinity stands for 32 NaNs.
+ * Scales: one byte each, log2(s) + 127 (255: the block stands for NaN), in
+ * tiles of 512 bytes for 128 rows x 128 columns: the byte of row r, columns
+ * 32 b .. 32 b + 31 of a tile is at 16 (r % 32) + 4 (r / 32) + b.  The tile of
+ * rows 128 i .. and columns 128 j .. is number i ceil(cols / 128) + j, so a
+ * matrix has lcvq_mx_scale_bytes(rows, cols) bytes of scales.  The bytes of
+ * rows beyond the last are neither written nor used; those of a row's columns
+ * beyond the last are written as 0. */
+typedef enum { LCVQ_MX4 = 0, LCVQ_MX8 = 1 } lcvq_mx_format;
 
 /* Code assignment and 2-bit packing (LC-QAT technical summary, Methodology 1:
  * index selection becomes rounding and clamping; Methodology 3: proxy weights
@@ -379,6 +404,69 @@ LCVQ_API lcvq_status lcvq_fit_affine_h(const float* W0, const uint8_t* packed, i
 LCVQ_API lcvq_status lcvq_assign_ldlq(const float* P, const float* U, int64_t d_out, int64_t d_in,
                                       int d, uint8_t* packed, void* workspace, size_t ws_bytes,
                                       void* stream);
+
+/* Packing into a block-scaled format (see lcvq_mx_format): activations in front
+ * of lcvq_mx4_gemm, weights once, activations kept for a backward.
+ *   X      [rows][cols] in `dtype`, row r at X + r * ld (ld in elements, >= cols).
+ *   q      [rows][cols/2] (MX4) or [rows][cols] (MX8) bytes out.
+ *   scales lcvq_mx_scale_bytes(rows, cols) bytes out.
+ * Shapes: cols % 32 == 0; every row 16-byte aligned (ld % 8 == 0 for bf16,
+ * ld % 4 == 0 for fp32); rows < 2^31, cols <= 2^30; rows * ceil(cols / 256) <
+ * 2^34.  rows == 0 or cols == 0 is a no-op.  Launches 1 kernel. */
+LCVQ_API lcvq_status lcvq_mx_pack(const void* X, lcvq_dtype dtype, int64_t rows, int64_t cols,
+                                  int64_t ld, lcvq_mx_format fmt, uint8_t* q, uint8_t* scales,
+                                  void* stream);
+/* The values a packed matrix stands for, exactly, in either dtype.
+ *   out [rows][cols] in `dtype`.  Shapes as lcvq_mx_pack. */
+LCVQ_API lcvq_status lcvq_mx_decode(const uint8_t* q, const uint8_t* scales, int64_t rows,
+                                    int64_t cols, lcvq_mx_format fmt, void* out, lcvq_dtype dtype,
+                                    void* stream);
+/* Bytes of the scales of a [rows][cols] matrix (0 on invalid input). */
+LCVQ_API size_t lcvq_mx_scale_bytes(int64_t rows, int64_t cols);
+
+/* Product of two MX4 matrices, Y[m][n] = sum_k X[m][k] W[n][k], for layers kept
+ * at 4 bits: activations from lcvq_mx_pack, weights packed once.  The products
+ * of a block are exact; they are scaled and summed in fp32 and rounded once to
+ * y_dtype.  A block that stands for NaN makes its row of Y (activations) or its
+ * column (weights) NaN.
+ *   X4 [M][d_in/2], SX its scales; W4 [d_out][d_in/2], SW its scales;
+ *   Y  [M][d_out] out in y_dtype.
+ *   workspace: >= lcvq_workspace_size(LCVQ_OP_MX4_GEMM, y_dtype, M, d_out, d_in, 8)
+ *   bytes, 256-byte aligned, first 256 bytes zeroed once (as lcvq_gemm).
+ * Shapes as lcvq_gemm.  M == 0 or d_out == 0 is a no-op; d_in == 0 writes
+ * Y = 0.  Launches 1 kernel.  Y must not overlap any input. */
+LCVQ_API lcvq_status lcvq_mx4_gemm(const uint8_t* X4, const uint8_t* SX, int64_t M,
+                                   const uint8_t* W4, const uint8_t* SW, int64_t d_out,
+                                   int64_t d_in, void* Y, lcvq_dtype y_dtype, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/* A training forward that keeps X at half its bytes: Y = X W~ exactly as
+ * lcvq_gemm computes it (form AUTO), and X packed into MX8 exactly as
+ * lcvq_mx_pack packs it (ld = d_in), for lcvq_gemm_backward_ckpt.
+ *   X8 [M][d_in] and S8 (lcvq_mx_scale_bytes(M, d_in) bytes) out; the rest as
+ *   lcvq_gemm.
+ *   workspace: >= lcvq_workspace_size(LCVQ_OP_GEMM_CKPT, dtype, M, d_out, d_in, d).
+ * Shapes as lcvq_gemm.  M == 0 or d_in == 0 keeps nothing; d_out == 0 keeps X. */
+LCVQ_API lcvq_status lcvq_gemm_ckpt(const void* X, lcvq_dtype dtype, int64_t M,
+                                    const uint8_t* packed, int64_t d_out, int64_t d_in, int d,
+                                    const float* A, const float* B, void* Y, uint8_t* X8,
+                                    uint8_t* S8, void* workspace, size_t ws_bytes, void* stream);
+
+/* lcvq_gemm_backward with X given as lcvq_gemm_ckpt (or lcvq_mx_pack with MX8)
+ * kept it: the gradients are those of the values it stands for, which enter
+ * exactly (they are bf16 values), so the only difference from the backward of
+ * the original X is the rounding of X to its block's grid, at most s / 2 =
+ * max|x| / 127 per element.  dX does not depend on X.  `dtype` is that of dY
+ * and dX.
+ *   workspace: >= lcvq_workspace_size(LCVQ_OP_GEMM_BACKWARD_CKPT, dtype, M,
+ *   d_out, d_in, d) bytes, 256-byte aligned, first 256 bytes zeroed once.
+ * Everything else as lcvq_gemm_backward. */
+LCVQ_API lcvq_status lcvq_gemm_backward_ckpt(const uint8_t* X8, const uint8_t* S8, const void* dY,
+                                             lcvq_dtype dtype, int64_t M, const uint8_t* packed,
+                                             const uint8_t* mask_bits, int64_t d_out, int64_t d_in,
+                                             int d, const float* A, const float* B, void* dX,
+                                             float* dA, float* dB, float* dWp, void* workspace,
+                                             size_t ws_bytes, void* stream);
 
 /* Workspace bytes a call with these arguments needs (0 on invalid input).
  * The workspace holds the device error word (its first 256 bytes, which the
