@@ -140,6 +140,11 @@ cudaError_t launch_mx4_gemv(const uint8_t* xq, const uint8_t* xs, int64_t M, con
                             const uint8_t* ws, int64_t N, int64_t K, void* Y, bool f32,
                             cudaStream_t s, int* launches);
 
+// the same on the block-scaled tensor-core MMA, tiles of 128 tokens x 192 rows
+cudaError_t launch_mx4_gemm(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
+                            const uint8_t* ws, int64_t N, int64_t K, void* Y, bool f32,
+                            unsigned int* err, cudaStream_t s, int* launches);
+
 // ---- tcgen05 GEMMs (bf16, persistent, one CTA per SM) ----
 int tc_max_grid();
 // Xa is X'' (algebraic, with corr) or X (decode form, A z + B decoded on chip)

@@ -306,6 +306,44 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
   return d;
 }
 
+// ---- block-scaled 4-bit floats (kind::mxf4: e2m1 elements, a power-of-two
+// scale byte per 32 elements).  The scales of an operand's rows are read from
+// TMEM: row r's word (four scale bytes) is lane r % 32 of column r / 32, in each
+// of the four lane quarters, which is what this copy of a 512-byte tile of 32
+// lanes x 16 bytes from shared memory gives.  It runs in order before MMAs that
+// the same thread issues after it.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// descriptor of such a tile: no swizzle, 8-row groups 128 bytes apart
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46);
+}
+// D[tmem] (+)= (A * scales of A) (B * scales of B)^T over 64 k, both K-major
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t a_scales, uint32_t b_scales, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::mxf4 (e2m1 A and B, power-of-two scales, K =
+// 64): `half` 0 or 1 takes bytes 0, 1 or 2, 3 of the scale words.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half) {
+  return (static_cast<uint32_t>(2 * half) << 4)      // B scale byte
+         | (1u << 7)                                 // A: e2m1
+         | (1u << 10)                                // B: e2m1
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (1u << 23)                                // scales: powers of two (ue8m0)
+         | (static_cast<uint32_t>(M >> 7) << 27)     // M / 128
+         | (static_cast<uint32_t>(2 * half) << 29);  // A scale byte
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16: bf16 A and B, fp32 D.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_major,
                                                       bool b_mn_major) {
