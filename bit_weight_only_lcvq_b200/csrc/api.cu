@@ -591,9 +591,10 @@ lcvq_status lcvq_mx4_gemm(const uint8_t* X4, const uint8_t* SX, int64_t M, const
     return LCVQ_ERR_WORKSPACE;
   if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
   int launches = 0;
-  cudaError_t e = M <= 32 ? launch_mx4_gemv(X4, SX, M, W4, SW, d_out, d_in, Y, f32, s, &launches)
-                          : launch_mx4_gemm(X4, SX, M, W4, SW, d_out, d_in, Y, f32,
-                                            static_cast<unsigned int*>(workspace), s, &launches);
+  cudaError_t e = M <= 128 ? launch_mx4_few(X4, SX, M, W4, SW, d_out, d_in, Y, f32,
+                                            static_cast<unsigned int*>(workspace), s, &launches)
+                           : launch_mx4_gemm(X4, SX, M, W4, SW, d_out, d_in, Y, f32,
+                                             static_cast<unsigned int*>(workspace), s, &launches);
   return finish(e, launches);
 }
 

@@ -134,13 +134,12 @@ cudaError_t launch_mx_pack(const void* X, bool f32, int64_t rows, int64_t cols, 
                            uint8_t* q, uint8_t* scales, cudaStream_t s, int* launches);
 cudaError_t launch_mx_decode(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
                              bool mx4, void* out, bool f32, cudaStream_t s, int* launches);
-// Y = X W^T of two mx4 matrices on the integer MMA, tiles of 16 rows of W and
-// up to 32 tokens
-cudaError_t launch_mx4_gemv(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
-                            const uint8_t* ws, int64_t N, int64_t K, void* Y, bool f32,
-                            cudaStream_t s, int* launches);
-
-// the same on the block-scaled tensor-core MMA, tiles of 128 tokens x 192 rows
+// Y = X W^T of two mx4 matrices on the block-scaled tensor-core MMA: M <= 128,
+// K split over a cluster
+cudaError_t launch_mx4_few(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
+                           const uint8_t* ws, int64_t N, int64_t K, void* Y, bool f32,
+                           unsigned int* err, cudaStream_t s, int* launches);
+// the same on CTA pairs, tiles of 256 tokens x 192 rows
 cudaError_t launch_mx4_gemm(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
                             const uint8_t* ws, int64_t N, int64_t K, void* Y, bool f32,
                             unsigned int* err, cudaStream_t s, int* launches);

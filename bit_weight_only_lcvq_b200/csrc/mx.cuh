@@ -20,8 +20,10 @@
 #pragma once
 
 #include "common.cuh"
+#include "internal.h"
 
 namespace lcvq {
+
 namespace mx {
 
 constexpr int kBlock = 32;
@@ -34,6 +36,14 @@ __host__ __device__ constexpr int64_t scale_bytes(int64_t rows, int64_t cols) {
 // byte offset of the 4-byte word with the scales of row r, columns 128 kt .. 128 kt + 127
 __host__ __device__ constexpr int64_t scale_word(int64_t r, int64_t kt, int64_t tiles_k) {
   return ((r >> 7) * tiles_k + kt) * kTileBytes + ((r & 31) << 4) + ((r >> 3) & 12);
+}
+
+// the scale tiles as a tensor of 512-byte rows, loaded two at a time (the two
+// tiles of 256 columns; past the end, zeros)
+inline bool make_scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t cols) {
+  return make_tensor_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, kTileBytes / 4,
+                            uint64_t(ceil_div(rows, 128) * scale_tiles_k(cols)), kTileBytes,
+                            kTileBytes / 4, 2, false);
 }
 
 // 2^(b - 127); byte 255 is NaN

@@ -386,37 +386,58 @@ def dge_scale(dWp: torch.Tensor, Wp: torch.Tensor, k: float, *, stream=None) -> 
 # ---- block-scaled formats (lcvq_mx_format in include/lcvq.h) ----
 # These calls take byte buffers whose meaning depends on shapes, so the binding
 # checks types, shapes and contiguity, and makes the tensors' device current.
+# A call's host time is a good part of a small operator's, so the checks are
+# kept to attribute reads and the stream is looked up once, without an object.
 
-def _need(t, name: str, dtype, shape, dev):
+_U8 = torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(i).cuda_stream, 3 us less
+
+
+def _wrong(t, name, dtype, shape, dev):
+    raise ValueError(f"lcvq: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     f"{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _need(t, name: str, dtype, shape, dev) -> int:
+    """The address of a tensor that is what the call needs it to be."""
     if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"lcvq: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t
+        _wrong(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
 
 def _ws(t, dev):
-    if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+    if t.dtype != _U8 or t.device != dev or not t.is_contiguous():
         raise ValueError(f"lcvq: the workspace must be a contiguous uint8 tensor on {dev}, got {t.dtype} "
                          f"on {t.device}")
     return t.data_ptr(), t.numel()
 
 
 def _mx_rows(t, name: str):
-    if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"lcvq: {name} must be a 2-D float32 or bfloat16 tensor, got {t.dtype} "
+    """(dtype code, rows, columns, device) of a 2-D fp32 or bf16 CUDA tensor."""
+    dt = t.dtype
+    if t.dim() != 2 or (dt != torch.bfloat16 and dt != torch.float32):
+        raise ValueError(f"lcvq: {name} must be a 2-D float32 or bfloat16 tensor, got {dt} "
                          f"{tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"lcvq: expected a CUDA tensor, got one on {t.device}")
+    rows, cols = t.shape
+    return (BF16 if dt == torch.bfloat16 else F32), rows, cols, t.device
 
 
-def _on_device(fn, name: str, dev, args, stream):
-    """fn(*args, stream) with dev current (the C ABI works on the current device)."""
-    if dev.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        return _check(name, fn(*args, s.cuda_stream))
-    with torch.cuda.device(dev):
-        s = torch.cuda.current_stream() if stream is None else stream
-        return _check(name, fn(*args, s.cuda_stream))
+def _on_device(name: str, dev, args, stream):
+    """The C call with dev current (the ABI works on the current device)."""
+    fn, i = getattr(_lib or lib(), name), dev.index
+    if i == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(i) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(i) if stream is None else stream.cuda_stream)
+    if st != 0:
+        raise LcvqError(name, st)
+
+
+def _tiles(rows: int, cols: int) -> int:
+    return -(-rows // 128) * -(-cols // 128) * 512
 
 
 def mx_scale_bytes(rows: int, cols: int) -> int:
@@ -427,23 +448,26 @@ def mx_scale_bytes(rows: int, cols: int) -> int:
 def mx_pack(X: torch.Tensor, fmt: str, *, q=None, scales=None, stream=None):
     """X [rows][cols] (fp32 or bf16, rows contiguous but possibly strided) packed
     into "mx4" or "mx8": (q, scales), see lcvq_mx_pack."""
-    _mx_rows(X, "X")
-    rows, cols = X.shape
-    f, dev = MX_FORMATS[fmt], X.device
+    dt, rows, cols, dev = _mx_rows(X, "X")
+    f = MX_FORMATS[fmt]
     if cols % 32:
         raise ValueError(f"lcvq: a block-scaled row has a multiple of 32 columns, got {cols}")
-    if cols and X.stride(1) != 1:
+    ld, inner = X.stride()
+    if inner != 1 and cols:
         raise ValueError("lcvq: the rows of X must be contiguous")
-    ld = X.stride(0) if rows > 1 else cols
-    qs, nb = (rows, cols // 2 if f == 0 else cols), -(-rows // 128) * -(-cols // 128) * 512
-    q = torch.empty(qs, dtype=torch.uint8, device=dev) if q is None else _need(q, "q", torch.uint8, qs, dev)
-    if scales is None:
-        scales = torch.empty(nb, dtype=torch.uint8, device=dev)
+    qc, nb = cols // 2 if f == 0 else cols, _tiles(rows, cols)
+    if q is None:
+        q = torch.empty(rows, qc, dtype=_U8, device=dev)
+        qp = q.data_ptr()
     else:
-        _need(scales, "scales", torch.uint8, (nb,), dev)
-    _on_device(lib().lcvq_mx_pack, "lcvq_mx_pack", dev,
-               (X.data_ptr(), _dtype_code(X.dtype), rows, cols, ld, f, q.data_ptr(), scales.data_ptr()),
-               stream)
+        qp = _need(q, "q", _U8, (rows, qc), dev)
+    if scales is None:
+        scales = torch.empty(nb, dtype=_U8, device=dev)
+        sp = scales.data_ptr()
+    else:
+        sp = _need(scales, "scales", _U8, (nb,), dev)
+    _on_device("lcvq_mx_pack", dev,
+               (X.data_ptr(), dt, rows, cols, ld if rows > 1 else cols, f, qp, sp), stream)
     return q, scales
 
 
@@ -453,15 +477,14 @@ def mx_decode(q: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str, *, dty
     if not q.is_cuda:
         raise ValueError(f"lcvq: expected a CUDA tensor, got one on {q.device}")
     f, dev, rows = MX_FORMATS[fmt], q.device, q.shape[0]
-    _need(q, "q", torch.uint8, (rows, cols // 2 if f == 0 else cols), dev)
-    _need(scales, "scales", torch.uint8, (-(-rows // 128) * -(-cols // 128) * 512,), dev)
+    qp = _need(q, "q", _U8, (rows, cols // 2 if f == 0 else cols), dev)
+    sp = _need(scales, "scales", _U8, (_tiles(rows, cols),), dev)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        out = torch.empty(rows, cols, dtype=dtype, device=dev)
+        op = out.data_ptr()
     else:
-        _need(out, "out", out.dtype, (rows, cols), dev)
-    _on_device(lib().lcvq_mx_decode, "lcvq_mx_decode", dev,
-               (q.data_ptr(), scales.data_ptr(), rows, cols, f, out.data_ptr(), _dtype_code(out.dtype)),
-               stream)
+        op = _need(out, "out", out.dtype, (rows, cols), dev)
+    _on_device("lcvq_mx_decode", dev, (qp, sp, rows, cols, f, op, _dtype_code(out.dtype)), stream)
     return out
 
 
@@ -472,56 +495,48 @@ def mx4_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Ten
     if not xq.is_cuda:
         raise ValueError(f"lcvq: expected a CUDA tensor, got one on {xq.device}")
     dev, (M, kb), N = xq.device, xq.shape, wq.shape[0]
-    kt = -(-kb // 64)
-    _need(xq, "xq", torch.uint8, (M, kb), dev)
-    _need(wq, "wq", torch.uint8, (N, kb), dev)
-    _need(xs, "xs", torch.uint8, (-(-M // 128) * kt * 512,), dev)
-    _need(ws, "ws", torch.uint8, (-(-N // 128) * kt * 512,), dev)
+    args = (_need(xq, "xq", _U8, (M, kb), dev), _need(xs, "xs", _U8, (_tiles(M, 2 * kb),), dev), M,
+            _need(wq, "wq", _U8, (N, kb), dev), _need(ws, "ws", _U8, (_tiles(N, 2 * kb),), dev), N, 2 * kb)
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=dev)
+        out = torch.empty(M, N, dtype=dtype, device=dev)
+        op = out.data_ptr()
     else:
-        _need(out, "out", out.dtype, (M, N), dev)
+        op = _need(out, "out", out.dtype, (M, N), dev)
     if workspace is None:
         workspace = new_workspace(workspace_size(OP_MX4_GEMM, out.dtype, M, N, 2 * kb, 8), dev)
-    _on_device(lib().lcvq_mx4_gemm, "lcvq_mx4_gemm", dev,
-               (xq.data_ptr(), xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, 2 * kb,
-                out.data_ptr(), _dtype_code(out.dtype), *_ws(workspace, dev)), stream)
+    _on_device("lcvq_mx4_gemm", dev, (*args, op, _dtype_code(out.dtype), *_ws(workspace, dev)), stream)
     return out
 
 
 def _layer(packed, d_in, A, B, d, dev):
     d_out = packed.shape[0]
-    _need(packed, "packed", torch.uint8, (d_out, d_in // 4), dev)
-    _need(A, "A", torch.float32, (d, d), dev)
-    _need(B, "B", torch.float32, (d,), dev)
-    return d_out
+    return (_need(packed, "packed", _U8, (d_out, d_in // 4), dev), d_out,
+            _need(A, "A", torch.float32, (d, d), dev), _need(B, "B", torch.float32, (d,), dev))
 
 
 def gemm_ckpt(X: torch.Tensor, packed: torch.Tensor, d_in: int, A: torch.Tensor, B: torch.Tensor,
               d: int, *, workspace=None, out=None, kept=None, stream=None):
     """Forward of a training step that keeps X in 8 bits: (Y, kept) with Y = X W~
-    as gemm computes it and kept = mx_pack(X, "mx8") for gemm_backward_ckpt."""
-    _mx_rows(X, "X")
-    dev, M = X.device, X.shape[0]
-    _need(X, "X", X.dtype, (M, d_in), dev)
-    d_out = _layer(packed, d_in, A, B, d, dev)
-    nb = -(-M // 128) * -(-d_in // 128) * 512
+    and kept = mx_pack(X, "mx8") for gemm_backward_ckpt (see lcvq_gemm_ckpt)."""
+    dt, M, _, dev = _mx_rows(X, "X")
+    xp = _need(X, "X", X.dtype, (M, d_in), dev)
+    pp, d_out, ap, bp = _layer(packed, d_in, A, B, d, dev)
+    nb = _tiles(M, d_in)
     if kept is None:
-        kept = (torch.empty((M, d_in), dtype=torch.uint8, device=dev),
-                torch.empty(nb, dtype=torch.uint8, device=dev))
+        kept = (torch.empty(M, d_in, dtype=_U8, device=dev), torch.empty(nb, dtype=_U8, device=dev))
+        qp, sp = kept[0].data_ptr(), kept[1].data_ptr()
     else:
-        _need(kept[0], "kept[0]", torch.uint8, (M, d_in), dev)
-        _need(kept[1], "kept[1]", torch.uint8, (nb,), dev)
+        qp = _need(kept[0], "kept[0]", _U8, (M, d_in), dev)
+        sp = _need(kept[1], "kept[1]", _U8, (nb,), dev)
     if out is None:
-        out = torch.empty((M, d_out), dtype=X.dtype, device=dev)
+        out = torch.empty(M, d_out, dtype=X.dtype, device=dev)
+        op = out.data_ptr()
     else:
-        _need(out, "out", X.dtype, (M, d_out), dev)
+        op = _need(out, "out", X.dtype, (M, d_out), dev)
     if workspace is None:
         workspace = new_workspace(workspace_size(OP_GEMM_CKPT, X.dtype, M, d_out, d_in, d), dev)
-    _on_device(lib().lcvq_gemm_ckpt, "lcvq_gemm_ckpt", dev,
-               (X.data_ptr(), _dtype_code(X.dtype), M, packed.data_ptr(), d_out, d_in, d, A.data_ptr(),
-                B.data_ptr(), out.data_ptr(), kept[0].data_ptr(), kept[1].data_ptr(),
-                *_ws(workspace, dev)), stream)
+    _on_device("lcvq_gemm_ckpt", dev,
+               (xp, dt, M, pp, d_out, d_in, d, ap, bp, op, qp, sp, *_ws(workspace, dev)), stream)
     return out, kept
 
 
@@ -530,31 +545,34 @@ def gemm_backward_ckpt(kept, dY: torch.Tensor, packed: torch.Tensor, mask, d_in:
                        want_dwp: bool = True, workspace=None, outs=None, stream=None) -> dict:
     """gemm_backward with X as gemm_ckpt kept it: dict(dX, dA, dB, dWp) (dX / dWp
     None when not wanted; mask may be None then)."""
-    _mx_rows(dY, "dY")
-    dev, M = dY.device, dY.shape[0]
-    d_out = _layer(packed, d_in, A, B, d, dev)
-    _need(dY, "dY", dY.dtype, (M, d_out), dev)
-    _need(kept[0], "kept[0]", torch.uint8, (M, d_in), dev)
-    _need(kept[1], "kept[1]", torch.uint8, (-(-M // 128) * -(-d_in // 128) * 512,), dev)
-    if mask is not None:
-        _need(mask, "mask", torch.uint8, (d_out, d_in // 8), dev)
-    o = dict(outs or {})
-    want = {"dX": ((M, d_in), dY.dtype, want_dx), "dWp": ((d_out, d_in), torch.float32, want_dwp),
-            "dA": ((d, d), torch.float32, True), "dB": ((d,), torch.float32, True)}
-    for k, (shape, dtype, wanted) in want.items():
-        if not wanted:
-            o[k] = None
-        elif o.get(k) is None:
-            o[k] = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _need(o[k], k, dtype, shape, dev)
+    dt, M, _, dev = _mx_rows(dY, "dY")
+    pp, d_out, ap, bp = _layer(packed, d_in, A, B, d, dev)
+    yp = _need(dY, "dY", dY.dtype, (M, d_out), dev)
+    qp = _need(kept[0], "kept[0]", _U8, (M, d_in), dev)
+    sp = _need(kept[1], "kept[1]", _U8, (_tiles(M, d_in),), dev)
+    mp = None if mask is None else _need(mask, "mask", _U8, (d_out, d_in // 8), dev)
+    o = dict(outs) if outs else {}
+
+    def result(k, dtype, *shape):
+        t = o.get(k)
+        if t is None:
+            t = o[k] = torch.empty(*shape, dtype=dtype, device=dev)
+            return t.data_ptr()
+        return _need(t, k, dtype, shape, dev)
+    xp = wp = None
+    if want_dx:
+        xp = result("dX", dY.dtype, M, d_in)
+    else:
+        o["dX"] = None
+    if want_dwp:
+        wp = result("dWp", torch.float32, d_out, d_in)
+    else:
+        o["dWp"] = None
     if workspace is None:
         workspace = new_workspace(
             workspace_size(OP_GEMM_BACKWARD_CKPT, dY.dtype, M, d_out, d_in, d), dev)
-    ptr = {k: None if o[k] is None else o[k].data_ptr() for k in want}
-    _on_device(lib().lcvq_gemm_backward_ckpt, "lcvq_gemm_backward_ckpt", dev,
-               (kept[0].data_ptr(), kept[1].data_ptr(), dY.data_ptr(), _dtype_code(dY.dtype), M,
-                packed.data_ptr(), None if mask is None else mask.data_ptr(), d_out, d_in, d,
-                A.data_ptr(), B.data_ptr(), ptr["dX"], ptr["dA"], ptr["dB"], ptr["dWp"],
+    _on_device("lcvq_gemm_backward_ckpt", dev,
+               (qp, sp, yp, dt, M, pp, mp, d_out, d_in, d, ap, bp, xp,
+                result("dA", torch.float32, d, d), result("dB", torch.float32, d), wp,
                 *_ws(workspace, dev)), stream)
     return o
