@@ -17,7 +17,7 @@
 // reads 7 KB.  Why 192 columns: two accumulators of 192, so that a tile's epilogue
 // overlaps the next tile's MMAs, leave 128 columns of TMEM for scales, 24 for
 // each 256 positions; two accumulators of 256 would leave none.  The scales have
-// five slots and the ring seven stages: before a slot is rewritten its MMAs, five
+// five slots and the ring six stages: before a slot is rewritten its MMAs, five
 // blocks back, have completed (the same barrier that frees their stage).
 //
 // A 192-row tile of weights starts at row 0 or 64 of a 128-row scale tile and
@@ -38,7 +38,7 @@ namespace {
 constexpr int BM = 128;            // tokens per CTA, 256 per pair
 constexpr int BN = 192;            // weight rows per pair, 96 loaded by each CTA
 constexpr int BK = 256;            // positions per stage: 128 bytes a row
-constexpr int STAGES = 7;
+constexpr int STAGES = 6;
 constexpr int A_BYTES = BM * 128;
 constexpr int B_BYTES = BN / 2 * 128;
 constexpr int SF_BYTES = 6 * mx::kTileBytes;  // A: 2 tiles (k); B: 2 (rows) x 2 (k)
@@ -50,11 +50,12 @@ constexpr int kTmemCols = 512;
 static_assert(2 * BN + SF_SLOTS * SF_COLS <= kTmemCols, "accumulators and scales fit TMEM");
 static_assert(SF_SLOTS <= STAGES, "a slot's MMAs free a stage that has not been filled again");
 constexpr int kThreads = 32 * 7;
-constexpr size_t kSmemBytes = 1024 + size_t(STAGES) * STAGE_BYTES + 256;
+// epilogue: two buffers of 32 rows x 128 bytes per warp
+constexpr int OUT_BYTES = 32 * 128;
+constexpr size_t kSmemBytes = 1024 + size_t(STAGES) * STAGE_BYTES + 8 * OUT_BYTES + 256;
 
 struct Params {
   int64_t M, N, K;
-  void* Y;
   unsigned int* err;
 };
 
@@ -67,10 +68,11 @@ template <bool kF32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
-                    const Params p) {
+                    const __grid_constant__ CUtensorMap tmY, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + size_t(STAGES) * STAGE_BYTES);
+  uint8_t* out = smem + size_t(STAGES) * STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out + 8 * OUT_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* sfull = empty + STAGES;  // even CTA: the stage's scales are in TMEM
   uint64_t* tfull = sfull + STAGES;
@@ -112,6 +114,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&tmB);
     tma_prefetch_map(&tmSa);
     tma_prefetch_map(&tmSb);
+    tma_prefetch_map(&tmY);
   }
   tc_fence_before();
   __syncthreads();
@@ -271,9 +274,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
+    // A warp's 32 rows leave in tiles of 128 bytes a row: written to shared memory
+    // in the SW128 order (a row per lane, chunks permuted: no bank conflicts) and
+    // stored by TMA, which clips what lies outside Y.  (Stored from registers, 16
+    // bytes a lane in 32 different rows, Y set the pace: 53 us against X us.)
+    constexpr int kCols = kF32 ? 32 : 64;
     const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;
+    const uint32_t buf0 = smem_u32(out) + quarter * 2 * OUT_BYTES;
     int64_t local = 0;
+    int ob = 0;
     for (int64_t tile = pair; tile < tiles && !warp_abort(); tile += npairs, ++local) {
       int64_t mt, nt;
       coords(tile, mt, nt);
@@ -284,38 +293,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const int64_t m = mt * 2 * BM + int64_t(rank) * BM + row;
+      const int64_t m = mt * 2 * BM + int64_t(rank) * BM + quarter * 32;
       const uint32_t tbase = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tbase + c * 32, r);
-        tmem_ld_wait();
-        const int64_t n0 = nt * BN + c * 32;
-        if (m >= p.M) continue;
+      for (int c = 0; c < BN / kCols; ++c) {
+        uint32_t r[kCols];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {  // N is a multiple of 8
-          if (n0 + 8 * q >= p.N) break;
-          if constexpr (kF32) {
-            float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.Y) + m * p.N + n0 + 8 * q);
-            y[0] = make_float4(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1]),
-                               __uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]));
-            y[1] = make_float4(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]),
-                               __uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7]));
-          } else {
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1]));
-            v.y = pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]));
-            v.z = pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]));
-            v.w = pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7]));
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.Y) + m * p.N + n0 + 8 * q) = v;
-          }
+        for (int h = 0; h < kCols / 32; ++h)
+          tmem_ld32(tbase + c * kCols + 32 * h, reinterpret_cast<uint32_t(&)[32]>(r[32 * h]));
+        tmem_ld_wait();
+        if (c == BN / kCols - 1) {  // the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
         }
+        if (lane == 0) bulk_wait_read<1>();  // the store before last has left this buffer
+        __syncwarp();
+        const uint32_t line = buf0 + ob * OUT_BYTES + lane * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint4 v;
+          if constexpr (kF32)
+            v = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+          else
+            v = make_uint4(pack_bf16x2(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1])),
+                           pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3])),
+                           pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5])),
+                           pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])));
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(line + ((q ^ (lane & 7)) << 4)),
+                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        fence_async_smem();
+        __syncwarp();
+        const int64_t n = nt * BN + c * kCols;
+        if (lane == 0) {
+          if (m < p.M && n < p.N)
+            tma_store_2d(&tmY, buf0 + ob * OUT_BYTES, static_cast<int>(n), static_cast<int>(m));
+          bulk_commit();
+        }
+        ob ^= 1;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -332,10 +353,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 cudaError_t launch_mx4_gemm(const uint8_t* xq, const uint8_t* xs, int64_t M, const uint8_t* wq,
                             const uint8_t* ws, int64_t N, int64_t K, void* Y, bool f32,
                             unsigned int* err, cudaStream_t s, int* launches) {
-  CUtensorMap ta, tb, sa, sb;
+  CUtensorMap ta, tb, sa, sb, ty;
   if (!make_tensor_map_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, xq, K / 2, M, K / 2, 128, BM, true) ||
       !make_tensor_map_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, wq, K / 2, N, K / 2, 128, BN / 2, true) ||
-      !mx::make_scale_map(&sa, xs, M, K) || !mx::make_scale_map(&sb, ws, N, K))
+      !mx::make_scale_map(&sa, xs, M, K) || !mx::make_scale_map(&sb, ws, N, K) ||
+      !make_tensor_map_2d(&ty, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, M,
+                          N * (f32 ? 4 : 2), f32 ? 32 : 64, 32, true))
     return cudaErrorInvalidValue;
   auto kern = f32 ? mx4_gemm_kernel<true> : mx4_gemm_kernel<false>;
   if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kSmemBytes);
@@ -343,7 +366,7 @@ cudaError_t launch_mx4_gemm(const uint8_t* xq, const uint8_t* xs, int64_t M, con
     return e;
   const int64_t tiles = ceil_div(M, 2 * BM) * ceil_div(N, BN);
   const int64_t pairs = tiles < tc_max_grid() / 2 ? tiles : tc_max_grid() / 2;
-  const Params p{M, N, K, Y, err};
+  const Params p{M, N, K, err};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -355,7 +378,7 @@ cudaError_t launch_mx4_gemm(const uint8_t* xq, const uint8_t* xs, int64_t M, con
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   ++*launches;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta, tb, sa, sb, p); e != cudaSuccess) return e;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ta, tb, sa, sb, ty, p); e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
