@@ -113,28 +113,30 @@ __global__ void __launch_bounds__(kThreads)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      int64_t issued = 0;
-      for (int64_t i = 0; i < kblocks; ++i) {
-        if (!mbar_wait(&empty[s], ph ^ 1, lim)) { fail(41); break; }
-        if (*abort_flag) break;
-        ++issued;
-        const int64_t kb = split + i * splits;
+    int s = 0;
+    uint32_t ph = 0;
+    int64_t issued = 0;
+    // two scale tiles per block (the second, past the last column, is not used)
+    const int sw0 = static_cast<int>(tile * tiles_k);
+    for (int64_t i = 0; i < kblocks; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1, lim))) { fail(41); break; }
+      if (__shfl_sync(0xffffffffu, *abort_flag, 0) != 0) break;
+      const int kb = static_cast<int>(split + i * splits);
+      uint8_t* st = smem + size_t(s) * C::kStage;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&full[s], C::kStage);
-        uint8_t* st = smem + size_t(s) * C::kStage;
-        tma_load_2d(&tmW, &full[s], st, static_cast<int>(kb) * 128, static_cast<int>(tile) * kRows);
-        tma_load_2d(&tmX, &full[s], st + C::kW, static_cast<int>(kb) * 128, 0);
-        // two scale tiles each (the second, past the last column, is not used)
-        tma_load_2d(&tmSw, &full[s], st + C::kW + C::kX, 0, static_cast<int>(tile * tiles_k + 2 * kb));
-        tma_load_2d(&tmSx, &full[s], st + C::kW + C::kX + 1024, 0, static_cast<int>(2 * kb));
-        if (++s == C::kStages) { s = 0; ph ^= 1; }
+        tma_load_2d(&tmW, &full[s], st, kb * 128, static_cast<int>(tile) * kRows);
+        tma_load_2d(&tmX, &full[s], st + C::kW, kb * 128, 0);
+        tma_load_2d(&tmSw, &full[s], st + C::kW + C::kX, 0, sw0 + 2 * kb);
+        tma_load_2d(&tmSx, &full[s], st + C::kW + C::kX + 1024, 0, 2 * kb);
       }
-      if (*abort_flag) {  // no copy may land in shared memory after the CTA exits
-        for (int64_t n = issued - 1; n >= 0 && n >= issued - C::kStages; --n)
-          mbar_wait(&full[n % C::kStages], static_cast<uint32_t>((n / C::kStages) & 1), kDefaultWaitLimit);
-      }
+      __syncwarp();
+      ++issued;
+      if (++s == C::kStages) { s = 0; ph ^= 1; }
+    }
+    if (__shfl_sync(0xffffffffu, *abort_flag, 0) != 0) {  // no copy may land in shared memory after the CTA exits
+      for (int64_t n = issued - 1; n >= 0 && n >= issued - C::kStages; --n)
+        mbar_wait(&full[n % C::kStages], static_cast<uint32_t>((n / C::kStages) & 1), kDefaultWaitLimit);
     }
   } else if (warp == 1) {
     constexpr uint32_t idesc0 = idesc_mxf4(kRows, NT, 0), idesc1 = idesc_mxf4(kRows, NT, 1);

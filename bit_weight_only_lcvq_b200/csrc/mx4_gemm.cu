@@ -134,41 +134,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      int64_t issued = 0;
-      for (int64_t tile = pair; tile < tiles && !*abort_flag; tile += npairs) {
-        int64_t mt, nt;
-        coords(tile, mt, nt);
-        const int64_t w0 = nt * BN >> 7;  // first scale tile of the weight rows
-        for (int64_t kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1, lim)) { fail(p, abort_flag, 31); break; }
-          if (*abort_flag) break;
-          ++issued;
-          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+    // the even CTA's full barriers and this CTA's stages as shared addresses: the
+    // operands of the copies stay uniform over the warp (see elect_one)
+    const uint32_t bar0 = mapa_shared(smem_u32(full), 0), st0 = smem_u32(smem);
+    int s = 0;
+    uint32_t ph = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t tile = pair; tile < tiles && ok; tile += npairs) {
+      int64_t mt, nt;
+      coords(tile, mt, nt);
+      const int row_a = static_cast<int>(mt * 2 * BM + rank * BM);
+      const int row_b = static_cast<int>(nt * BN + rank * (BN / 2));
+      // two scale tiles per block (the second, past the last column, is not used;
+      // tiles past the last row scale rows of D that are not stored)
+      const int64_t w0 = nt * BN >> 7;  // first scale tile of the weight rows
+      int sa = static_cast<int>((mt * 2 + rank) * tiles_k), sb = static_cast<int>(w0 * tiles_k);
+      const int sb_next = static_cast<int>(tiles_k);
+      for (int kb = 0; kb < static_cast<int>(kblocks); ++kb, sa += 2, sb += 2) {
+        const bool free_stage = mbar_wait(&empty[s], ph ^ 1, lim);
+        if (!__all_sync(0xffffffffu, free_stage)) { fail(p, abort_flag, 31); ok = false; break; }
+        if (warp_abort()) { ok = false; break; }
+        const uint32_t bar = bar0 + 8 * s, st = st0 + s * STAGE_BYTES, sf = st + A_BYTES + B_BYTES;
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
-          uint8_t* st = smem + size_t(s) * STAGE_BYTES;
-          uint8_t* sf = st + A_BYTES + B_BYTES;
-          tma_load_2d_pair(&tmA, bar, st, static_cast<int>(kb) * 128,
-                           static_cast<int>(mt * 2 * BM + rank * BM));
-          tma_load_2d_pair(&tmB, bar, st + A_BYTES, static_cast<int>(kb) * 128,
-                           static_cast<int>(nt * BN + rank * (BN / 2)));
-          // two scale tiles each (the second, past the last column, is not used;
-          // tiles past the last row scale rows of D that are not stored)
-          tma_load_2d_pair(&tmSa, bar, sf, 0, static_cast<int>((mt * 2 + rank) * tiles_k + 2 * kb));
-          tma_load_2d_pair(&tmSb, bar, sf + 1024, 0, static_cast<int>(w0 * tiles_k + 2 * kb));
-          tma_load_2d_pair(&tmSb, bar, sf + 2048, 0, static_cast<int>((w0 + 1) * tiles_k + 2 * kb));
-          if (++s == STAGES) { s = 0; ph ^= 1; }
+          tma_load_2d_pair(&tmA, bar, st, kb * 128, row_a);
+          tma_load_2d_pair(&tmB, bar, st + A_BYTES, kb * 128, row_b);
+          tma_load_2d_pair(&tmSa, bar, sf, 0, sa);
+          tma_load_2d_pair(&tmSb, bar, sf + 1024, 0, sb);
+          tma_load_2d_pair(&tmSb, bar, sf + 2048, 0, sb + sb_next);
         }
+        __syncwarp();
+        ++issued;
+        if (++s == STAGES) { s = 0; ph ^= 1; }
       }
-      if (*abort_flag && rank == 0) {
-        // no copy may land in shared memory after the CTA exits: the even CTA's
-        // barriers count the bytes of both, and neither CTA leaves before the
-        // cluster barrier at the end
-        for (int64_t n = issued - 1; n >= 0 && n >= issued - STAGES; --n)
-          mbar_wait(&full[n % STAGES], static_cast<uint32_t>((n / STAGES) & 1), kDefaultWaitLimit);
-      }
+    }
+    if (warp_abort() && rank == 0) {
+      // no copy may land in shared memory after the CTA exits: the even CTA's
+      // barriers count the bytes of both, and neither CTA leaves before the
+      // cluster barrier at the end
+      for (int64_t n = issued - 1; n >= 0 && n >= issued - STAGES; --n)
+        mbar_wait(&full[n % STAGES], static_cast<uint32_t>((n / STAGES) & 1), kDefaultWaitLimit);
     }
   } else if (warp == 1) {
     if (rank == 0) {

@@ -179,12 +179,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 // 2D tile load by one CTA of a CTA pair; completion is counted on `cluster_bar`,
 // which may be the peer CTA's mbarrier (shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* m, uint32_t cluster_bar,
-                                                 void* dst, int x, int y) {
+                                                 uint32_t dst, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4}], [%2];\n" ::"r"(smem_u32(dst)),
+      "[%0], [%1, {%3, %4}], [%2];\n" ::"r"(dst),
       "l"(m), "r"(cluster_bar), "r"(x), "r"(y)
       : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* m, uint32_t cluster_bar,
+                                                 void* dst, int x, int y) {
+  tma_load_2d_pair(m, cluster_bar, smem_u32(dst), x, y);
 }
 
 // One lane of a whole warp (the same one every time).  tcgen05 instructions take
