@@ -86,6 +86,16 @@ __device__ __forceinline__ uint32_t ld_global_u32(const void* p) {
   asm volatile("ld.global.u32 %0, [%1];\n" : "=r"(v) : "l"(p));
   return v;
 }
+__device__ __forceinline__ uint32_t ld_global_u16(const void* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];\n" : "=h"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_global_u8(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ float ld_global_f32(const float* p) {
   float v;
   asm volatile("ld.global.f32 %0, [%1];\n" : "=f"(v) : "l"(p));

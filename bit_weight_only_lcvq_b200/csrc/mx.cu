@@ -7,10 +7,11 @@
 // Both kernels are bound by HBM: packing reads 2 or 4 B an element and writes
 // 0.53 (mx4) or 1.03 (mx8), decoding the reverse.  A warp takes 256 consecutive
 // columns of one row at a time, eight elements a lane, so a block is four
-// neighbouring lanes and its maximum two shuffles; the four scale bytes of 128
-// columns meet in one lane and leave as one word.  kUnits such pieces are in
-// flight per warp where there is enough work to fill the GPU with four of them
-// (kUnitsMin below).
+// neighbouring lanes and its maximum two shuffles.  A warp has four such
+// pieces in flight where there is enough work to fill the GPU that way.
+// Measured on 8192 x 14336 (bytes read and written over time): mx8 from bf16 56 us
+// (6.4 TB/s), from fp32 83 (7.1); mx4 from bf16 51 (5.8), from fp32 76 (7.0);
+// decoding to bf16 54 and 47, to fp32 91 and 83 (6.4 to 6.6).
 #include "common.cuh"
 #include "gemv_common.cuh"
 #include "internal.h"
@@ -24,143 +25,193 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPiece = 256;  // columns per warp piece, 8 per lane
 
-// the eight elements of a lane, as fp32
+// Eight consecutive elements of a lane as they lie in memory (bf16: four words).
 template <bool kF32>
-__device__ __forceinline__ void load8(const void* X, int64_t off, float (&x)[8]) {
-  if constexpr (kF32) {
-    const uint4 a = ld_global_v4(static_cast<const float*>(X) + off);
-    const uint4 b = ld_global_v4(static_cast<const float*>(X) + off + 4);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+struct Eight {
+  uint32_t w[kF32 ? 8 : 4];
+
+  __device__ __forceinline__ void load(const char* at) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
-  } else {
-    const uint4 a = ld_global_v4(static_cast<const uint16_t*>(X) + off);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_lo(w[i]);
-      x[2 * i + 1] = bf16_hi(w[i]);
+    for (int i = 0; i < (kF32 ? 2 : 1); ++i) {
+      const uint4 v = ld_global_v4(at + 16 * i);
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
     }
   }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (kF32 ? 8 : 4); ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (kF32) return __uint_as_float(w[i]);
+    else return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+  }
+  // bits of the largest magnitude, as fp32 (integers order like magnitudes)
+  __device__ __forceinline__ uint32_t max_bits() const {
+    if constexpr (kF32) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+      uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+      for (int i = 1; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      return max(m << 16, m & 0xFFFF0000u);
+    }
+  }
+  // the top bytes (with the signs) of elements 4 g + 0, 2, 1, 3
+  __device__ __forceinline__ uint32_t signs(int g) const {
+    if constexpr (kF32)
+      return __byte_perm(__byte_perm(w[4 * g], w[4 * g + 2], 0x0073), __byte_perm(w[4 * g + 1], w[4 * g + 3], 0x0073), 0x5410);
+    else
+      return __byte_perm(w[2 * g], w[2 * g + 1], 0x7351);
+  }
+};
+
+// The packed form of eight elements: mx4 in .x, mx8 in .x and .y.
+template <bool kMx4, bool kF32>
+__device__ __forceinline__ uint2 pack8(const Eight<kF32>& x, uint32_t sb) {
+  const float inv = mx::scale_inverse(sb);
+  uint2 o = make_uint2(0, 0);
+  if (sb >= (kMx4 ? 253u : 249u)) {  // blocks that are not finite, and the highest binade
+    const float top = mx::element_top<kMx4>(sb);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = sb == 255u ? 0.f : fminf(fmaxf(x[i] * inv, -top), top);
+    if constexpr (kMx4) {
+      o.x = mx::e2m1_x4(v[0], v[1], v[2], v[3]) | mx::e2m1_x4(v[4], v[5], v[6], v[7]) << 16;
+    } else {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {  // byte b of a group of four holds element 0, 2, 1, 3
+        const int i = (b & 4) + ((b >> 1) & 1) + 2 * (b & 1);
+        const uint32_t c = (mx::mx8_bits(v[i], 1.f) & 0x7Fu) | (__float_as_uint(v[i]) >> 24 & 0x80u);
+        (b < 4 ? o.x : o.y) |= c << (8 * (b & 3));
+      }
+    }
+    return o;
+  }
+  if constexpr (kMx4) {
+    o.x = mx::e2m1_x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv) |
+          mx::e2m1_x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv) << 16;
+  } else {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = mx::mx8_bits(x[4 * g + i], inv);
+      const uint32_t m = __byte_perm(__byte_perm(u[0], u[2], 0x0040), __byte_perm(u[1], u[3], 0x0040), 0x5410);
+      (g ? o.y : o.x) = m | (x.signs(g) & 0x80808080u);
+    }
+  }
+  return o;
 }
 
+// A warp packs kUnits pieces of one row: `segs` such segments make a row.
 template <bool kMx4, bool kF32, int kUnits>
 __global__ void __launch_bounds__(kThreads)
-    mx_pack_kernel(const void* X, int64_t ld, int64_t cols, int64_t pieces_per_row, int64_t pieces,
+    mx_pack_kernel(const void* X, int64_t ld, int64_t rows, int64_t cols, int segs,
                    uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   // X may come from the kernel just before this one (see ld_global_v4)
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t first = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kUnits;
-  if (first >= pieces) return;
-  int64_t row = first / pieces_per_row, pc = first % pieces_per_row;
+  const int64_t seg = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t row = seg / segs;
+  if (row >= rows) return;
+  const int64_t c0 = (seg - row * segs) * (kUnits * kPiece) + 8 * lane;
   const int64_t tiles_k = mx::scale_tiles_k(cols);
-  float x[kUnits][8];
-  int64_t rows[kUnits], c0[kUnits];
+  const int left = static_cast<int>(cols - c0), pad = static_cast<int>(tiles_k * 128 - c0);
+  const char* src = static_cast<const char*>(X) + (row * ld + c0) * (kF32 ? 4 : 2);
+  Eight<kF32> x[kUnits];
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    rows[u] = first + u < pieces ? row : -1;
-    c0[u] = pc * kPiece + 8 * lane;
-    if (rows[u] >= 0 && c0[u] < cols) {
-      load8<kF32>(X, row * ld + c0[u], x[u]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-    }
-    if (++pc == pieces_per_row) { pc = 0; ++row; }
+    if (u * kPiece < left) x[u].load(src + u * kPiece * (kF32 ? 4 : 2));
+    else x[u].zero();
   }
+  uint8_t* dst = q + (kMx4 ? row * (cols / 2) + c0 / 2 : row * cols + c0);
+  uint8_t* sc = scales + mx::scale_word(row, c0 >> 7, tiles_k) + ((c0 >> 5) & 3);
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) {
-    if (rows[u] < 0) break;
-    const bool in = c0[u] < cols;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[u][i]) & 0x7FFFFFFFu);
+    uint32_t m = x[u].max_bits();
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t sb = mx::scale_byte<kMx4>(m);
-    const float inv = mx::scale_inverse(sb), top = mx::element_top<kMx4>(sb);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = fminf(fmaxf(x[u][i] * inv, -top), top);
-      if (sb == 255u) v[i] = 0.f;
-    }
+    const bool in = u * kPiece < left;
     if (in) {
-      if constexpr (kMx4) {
-        const uint32_t w = mx::e2m1_x4(v[0], v[1], v[2], v[3]) | mx::e2m1_x4(v[4], v[5], v[6], v[7]) << 16;
-        *reinterpret_cast<uint32_t*>(q + rows[u] * (cols / 2) + c0[u] / 2) = w;
-      } else {
-        uint2 w;  // bytes 0, 1, 2, 3 hold elements 0, 2, 1, 3
-        w.x = mx::mx8_code(v[0]) | mx::mx8_code(v[2]) << 8 | mx::mx8_code(v[1]) << 16 | mx::mx8_code(v[3]) << 24;
-        w.y = mx::mx8_code(v[4]) | mx::mx8_code(v[6]) << 8 | mx::mx8_code(v[5]) << 16 | mx::mx8_code(v[7]) << 24;
-        *reinterpret_cast<uint2*>(q + rows[u] * cols + c0[u]) = w;
-      }
+      const uint2 o = pack8<kMx4, kF32>(x[u], sb);
+      if constexpr (kMx4) *reinterpret_cast<uint32_t*>(dst + u * kPiece / 2) = o.x;
+      else *reinterpret_cast<uint2*>(dst + u * kPiece) = o;
     }
-    // the four blocks of 128 columns (lanes 0, 4, 8, 12 of each half warp)
-    uint32_t word = in ? sb << (8 * ((lane >> 2) & 3)) : 0u;
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if ((lane & 15) == 0 && in)
-      *reinterpret_cast<uint32_t*>(scales + mx::scale_word(rows[u], c0[u] >> 7, tiles_k)) = word;
+    // every fourth lane has a block; the blocks of a tile past the last column are 0
+    if ((lane & 3) == 0 && u * kPiece < pad) sc[u * (kPiece / 128) * mx::kTileBytes] = in ? sb : 0;
   }
 }
 
+// Decoding: a lane takes eight consecutive columns for bf16 and, for fp32, four in
+// either half of the piece, so that a warp's 16-byte stores are 512 consecutive
+// bytes (two stores to 32 bytes of a lane's own measured 121 us against 97 on
+// mx4, 8192 x 14336).
 template <bool kMx4, bool kF32, int kUnits>
 __global__ void __launch_bounds__(kThreads)
-    mx_decode_kernel(const uint8_t* q, const uint8_t* scales, int64_t cols, int64_t pieces_per_row,
-                     int64_t pieces, void* __restrict__ out) {
+    mx_decode_kernel(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols, int segs,
+                     void* __restrict__ out) {
   griddep_wait();
   griddep_launch_dependents();
+  constexpr int kParts = kF32 ? 2 : 1;
+  constexpr int kStep = kPiece / kParts;  // columns between a lane's parts
   const int lane = threadIdx.x & 31;
-  const int64_t first = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kUnits;
-  if (first >= pieces) return;
-  int64_t row = first / pieces_per_row, pc = first % pieces_per_row;
-  const int64_t tiles_k = mx::scale_tiles_k(cols);
-  uint2 w[kUnits];
-  uint32_t sb[kUnits];
-  int64_t at[kUnits];
+  const int64_t seg = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t row = seg / segs;
+  if (row >= rows) return;
+  const int64_t c0 = (seg - row * segs) * (kUnits * kPiece) + (kF32 ? 4 : 8) * lane;
+  const int left = static_cast<int>(cols - c0);
+  const uint8_t* src = q + (kMx4 ? row * (cols / 2) + c0 / 2 : row * cols + c0);
+  const uint8_t* sc = scales + mx::scale_word(row, c0 >> 7, mx::scale_tiles_k(cols)) + ((c0 >> 5) & 3);
+  char* dst = static_cast<char*>(out) + (row * cols + c0) * (kF32 ? 4 : 2);
+  uint2 w[kUnits * kParts];
+  uint32_t sb[kUnits * kParts];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int64_t c = pc * kPiece + 8 * lane;
-    at[u] = first + u < pieces && c < cols ? row * cols + c : -1;
+  for (int u = 0; u < kUnits * kParts; ++u) {
     w[u] = make_uint2(0, 0);
     sb[u] = 0;
-    if (at[u] >= 0) {
-      if constexpr (kMx4) w[u].x = ld_global_u32(q + at[u] / 2);
-      else w[u] = ld_global_v2(q + at[u]);
-      sb[u] = ld_global_u32(scales + mx::scale_word(row, c >> 7, tiles_k)) >> (8 * ((c >> 5) & 3)) & 255u;
+    if (u * kStep < left) {
+      if constexpr (kF32) w[u].x = kMx4 ? ld_global_u16(src + u * kStep / 2) : ld_global_u32(src + u * kStep);
+      else if constexpr (kMx4) w[u].x = ld_global_u32(src + u * kStep / 2);
+      else w[u] = ld_global_v2(src + u * kStep);
+      sb[u] = ld_global_u8(sc + u * (kStep / 128) * mx::kTileBytes);
     }
-    if (++pc == pieces_per_row) { pc = 0; ++row; }
   }
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    if (at[u] < 0) continue;
-    const float s = mx::scale_value(sb[u]);
-    float v[8];
-    if constexpr (kMx4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = mx::e2m1_value(w[u].x >> (4 * i)) * s;
-    } else {
-      auto value = [&](uint32_t b) {
-        const float m = static_cast<float>(b & 127u) * s;
-        return (b & 128u) ? -m : m;
-      };
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {  // element 4 g + 2 a + b is byte 4 g + a + 2 b
-        const int byte = (i & 4) + ((i >> 1) & 1) + 2 * (i & 1);
-        v[i] = value((byte < 4 ? w[u].x : w[u].y) >> (8 * (byte & 3)) & 255u);
-      }
-    }
+  for (int u = 0; u < kUnits * kParts; ++u) {
+    if (u * kStep >= left) break;
     if constexpr (kF32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at[u]);
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {  // exact: at most seven significant bits
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at[u]) =
-          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
+      const float s = mx::scale_value(sb[u]);
+      float4 o;
+      if constexpr (kMx4) {
+        const float2 a = mx::e2m1_values(w[u].x), b = mx::e2m1_values(w[u].x >> 8);
+        o = make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
+      } else {  // bytes 0, 1, 2, 3 hold elements 0, 2, 1, 3
+        o = make_float4(mx::mx8_value(w[u].x, s), mx::mx8_value(w[u].x >> 16, s),
+                        mx::mx8_value(w[u].x >> 8, s), mx::mx8_value(w[u].x >> 24, s));
+      }
+      *reinterpret_cast<float4*>(dst + u * kStep * 4) = o;
+    } else {
+      uint4 o;  // exact: products of at most seven significant bits with a power of two
+      if constexpr (kMx4) {
+        const float s = mx::scale_value(sb[u]);
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = mx::e2m1_values(w[u].x >> (8 * i));
+          p[i] = pack_bf16x2(f.x * s, f.y * s);
+        }
+        o = make_uint4(p[0], p[1], p[2], p[3]);
+      } else {
+        const uint32_t s2 = mx::scale_bf16x2(sb[u]);
+        mx::mx8_word_bf16(w[u].x, s2, o.x, o.y);
+        mx::mx8_word_bf16(w[u].y, s2, o.z, o.w);
+      }
+      *reinterpret_cast<uint4*>(dst + u * kStep * 2) = o;
     }
   }
 }
@@ -181,43 +232,48 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), int64_t grid, cudaStream_t s, Arg
   return cudaGetLastError();
 }
 
-// pieces from which a warp takes four at a time: two waves of eight resident
-// CTAs per SM with four pieces a warp; below, one piece a warp spreads the work
-// over more SMs
-constexpr int64_t kUnitsMin = int64_t(kNumSMsB200) * 8 * kWarps * 4 * 2;
+// Pieces of a row that a warp takes: four where that still gives two waves of
+// eight resident CTAs per SM; below, one, which spreads the work over more SMs.
+constexpr int kUnits = 4;
+int64_t segments(int64_t cols, int units) { return ceil_div(cols, int64_t(kPiece) * units); }
+bool many_segments(int64_t rows, int64_t cols) {
+  return rows * segments(cols, kUnits) >= int64_t(kNumSMsB200) * 8 * kWarps * 2;
+}
 
 }  // namespace
 
 cudaError_t launch_mx_pack(const void* X, bool f32, int64_t rows, int64_t cols, int64_t ld, bool mx4,
                            uint8_t* q, uint8_t* scales, cudaStream_t s, int* launches) {
-  const int64_t ppr = ceil_div(cols, kPiece), pieces = rows * ppr;
-  const bool many = pieces >= kUnitsMin;
-  const int64_t grid = ceil_div(pieces, kWarps * (many ? 4 : 1));
+  const bool many = many_segments(rows, cols);
+  const int64_t segs = segments(cols, many ? kUnits : 1), grid = ceil_div(rows * segs, kWarps);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  auto go = [&](auto kern) { return launch_pdl(kern, grid, s, X, ld, cols, ppr, pieces, q, scales); };
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, grid, s, X, ld, rows, cols, static_cast<int>(segs), q, scales);
+  };
   ++*launches;
   if (mx4) {
-    if (f32) return many ? go(mx_pack_kernel<true, true, 4>) : go(mx_pack_kernel<true, true, 1>);
-    return many ? go(mx_pack_kernel<true, false, 4>) : go(mx_pack_kernel<true, false, 1>);
+    if (f32) return many ? go(mx_pack_kernel<true, true, kUnits>) : go(mx_pack_kernel<true, true, 1>);
+    return many ? go(mx_pack_kernel<true, false, kUnits>) : go(mx_pack_kernel<true, false, 1>);
   }
-  if (f32) return many ? go(mx_pack_kernel<false, true, 4>) : go(mx_pack_kernel<false, true, 1>);
-  return many ? go(mx_pack_kernel<false, false, 4>) : go(mx_pack_kernel<false, false, 1>);
+  if (f32) return many ? go(mx_pack_kernel<false, true, kUnits>) : go(mx_pack_kernel<false, true, 1>);
+  return many ? go(mx_pack_kernel<false, false, kUnits>) : go(mx_pack_kernel<false, false, 1>);
 }
 
 cudaError_t launch_mx_decode(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
                              bool mx4, void* out, bool f32, cudaStream_t s, int* launches) {
-  const int64_t ppr = ceil_div(cols, kPiece), pieces = rows * ppr;
-  const bool many = pieces >= kUnitsMin;
-  const int64_t grid = ceil_div(pieces, kWarps * (many ? 4 : 1));
+  const bool many = many_segments(rows, cols);
+  const int64_t segs = segments(cols, many ? kUnits : 1), grid = ceil_div(rows * segs, kWarps);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  auto go = [&](auto kern) { return launch_pdl(kern, grid, s, q, scales, cols, ppr, pieces, out); };
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, grid, s, q, scales, rows, cols, static_cast<int>(segs), out);
+  };
   ++*launches;
   if (mx4) {
-    if (f32) return many ? go(mx_decode_kernel<true, true, 4>) : go(mx_decode_kernel<true, true, 1>);
-    return many ? go(mx_decode_kernel<true, false, 4>) : go(mx_decode_kernel<true, false, 1>);
+    if (f32) return many ? go(mx_decode_kernel<true, true, kUnits>) : go(mx_decode_kernel<true, true, 1>);
+    return many ? go(mx_decode_kernel<true, false, kUnits>) : go(mx_decode_kernel<true, false, 1>);
   }
-  if (f32) return many ? go(mx_decode_kernel<false, true, 4>) : go(mx_decode_kernel<false, true, 1>);
-  return many ? go(mx_decode_kernel<false, false, 4>) : go(mx_decode_kernel<false, false, 1>);
+  if (f32) return many ? go(mx_decode_kernel<false, true, kUnits>) : go(mx_decode_kernel<false, true, 1>);
+  return many ? go(mx_decode_kernel<false, false, kUnits>) : go(mx_decode_kernel<false, false, 1>);
 }
 
 }  // namespace lcvq

@@ -19,6 +19,8 @@
 // moves there with one bulk copy.  Tiles lie row of tiles after row of tiles.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -90,21 +92,29 @@ __device__ __forceinline__ uint32_t e2m1_x4(float x0, float x1, float x2, float 
       : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
   return r;
 }
-// one fp32 already divided by the scale -> sign-and-magnitude byte: adding 2^23
-// leaves the magnitude, rounded to nearest even, in the low mantissa bits
-__device__ __forceinline__ uint32_t mx8_code(float x) {
-  const uint32_t u = __float_as_uint(x);
-  const uint32_t m = __float_as_uint(fabsf(x) + 8388608.f) & 0x7Fu;
-  return m | ((u >> 24) & 0x80u);
+// bits of 2^23 + |x| inv: its low byte is the magnitude |x| / s <= 127, rounded
+// to nearest even by the one rounding of the fused multiply-add
+__device__ __forceinline__ uint32_t mx8_bits(float x, float inv) {
+  return __float_as_uint(fmaf(fabsf(x), inv, 8388608.f));
 }
 
-// value of one e2m1 nibble (in units of the scale)
-__device__ __forceinline__ float e2m1_value(uint32_t n) {
-  const uint32_t mag = n & 7u;
-  // exponent 0: 0 or 0.5; otherwise (1 + m / 2) 2^(e - 1)
-  const float v = mag < 2u ? 0.5f * static_cast<float>(mag)
-                           : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
-  return (n & 8u) ? -v : v;
+// value of the mx8 byte in bits 0 .. 7 of w, times the scale (exact)
+__device__ __forceinline__ float mx8_value(uint32_t w, float s) {
+  const float m = (__uint_as_float(0x4B000000u | (w & 0x7Fu)) - 8388608.f) * s;
+  return __uint_as_float(__float_as_uint(m) ^ (w << 24 & 0x80000000u));
+}
+
+// two e2m1 nibbles (the low byte of w) -> their values (in units of the scale)
+__device__ __forceinline__ float2 e2m1_values(uint32_t w) {
+  uint32_t h;
+  asm("{\n"
+      ".reg .b8 b0, b1, b2, b3;\n"
+      "mov.b32 {b0, b1, b2, b3}, %1;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+      "}\n"
+      : "=r"(h)
+      : "r"(w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // Four mx8 bytes (one word) -> elements 0, 1 and 2, 3 as bf16 pairs, times the

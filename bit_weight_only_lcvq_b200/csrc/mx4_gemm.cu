@@ -283,7 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // A warp's 32 rows leave in tiles of 128 bytes a row: written to shared memory
     // in the SW128 order (a row per lane, chunks permuted: no bank conflicts) and
     // stored by TMA, which clips what lies outside Y.  (Stored from registers, 16
-    // bytes a lane in 32 different rows, Y set the pace: 53 us against X us.)
+    // bytes a lane in 32 different rows, Y set the pace:
+    // 53 us against 47 at 2048 x 4096 -> 11008.)
     constexpr int kCols = kF32 ? 32 : 64;
     const int quarter = warp & 3;
     const uint32_t buf0 = smem_u32(out) + quarter * 2 * OUT_BYTES;
