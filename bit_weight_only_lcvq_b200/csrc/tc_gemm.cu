@@ -307,19 +307,25 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      int64_t issued = 0;
-      for (int64_t tile = blockIdx.x; tile < tiles && !*abort_flag; tile += gridDim.x) {
-        int mt, nt;
-        tile_coords(tile, m_tiles, n_tiles, kBand, mt, nt);
-        for (int64_t kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1, lim)) { fail(p, abort_flag, 1); break; }
-          if (*abort_flag) break;
-          ++issued;
+    // (the whole warp runs the loop; an elected lane issues, see elect_one)
+    int s = 0;
+    uint32_t ph = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      int mt, nt;
+      tile_coords(tile, m_tiles, n_tiles, kBand, mt, nt);
+      for (int64_t kb = 0; kb < kblocks; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1, lim))) {
+          fail(p, abort_flag, 1);
+          ok = false;
+          break;
+        }
+        if (warp_abort()) { ok = false; break; }
+        ++issued;
+        const int kx = static_cast<int>(kb);
+        if (elect_one()) {
           mbar_arrive_expect_tx(&full[s], C::kStageTx);
-          const int kx = static_cast<int>(kb);
           if constexpr (KIND == kFwdAlg || KIND == kFwdDec) {
             tma_load_2d(&tmA, &full[s], sA + s * A_BYTES, kx * BK, mt * BM);
             tma_load_2d(&tmB, &full[s], sC + s * C_BYTES, kx * (BK / 4), nt * BN);
@@ -333,36 +339,43 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
             for (int q = 0; q < 4; ++q)
               tma_load_2d(&tmB, &full[s], sB + s * B_BYTES + q * 8192, nt * BN + q * 64, kx * BK);
           }
-          if (++s == STAGES) { s = 0; ph ^= 1; }
         }
+        __syncwarp();
+        if (++s == STAGES) { s = 0; ph ^= 1; }
       }
-      if (*abort_flag) {  // no copy may land in shared memory after the CTA exits
-        // (the default limit: copies in flight finish in microseconds)
-        for (int64_t n = issued - 1; n >= 0 && n >= issued - STAGES; --n)
-          mbar_wait(&full[n % STAGES], static_cast<uint32_t>((n / STAGES) & 1), kDefaultWaitLimit);
-      }
+    }
+    if (warp_abort()) {  // no copy may land in shared memory after the CTA exits
+      // (the default limit: copies in flight finish in microseconds)
+      for (int64_t n = issued - 1; n >= 0 && n >= issued - STAGES; --n)
+        mbar_wait(&full[n % STAGES], static_cast<uint32_t>((n / STAGES) & 1), kDefaultWaitLimit);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, C::kAmn, C::kBmn);
-      int s = 0;
-      uint32_t ph = 0;
-      int64_t local = 0;
-      bool issued = false;
-      for (int64_t tile = blockIdx.x; tile < tiles && !*abort_flag; tile += gridDim.x, ++local) {
-        const int buf = static_cast<int>(local & 1);
-        const uint32_t use = static_cast<uint32_t>(local >> 1);
-        if (!mbar_wait(&tempty[buf], (use & 1) ^ 1, lim)) { fail(p, abort_flag, 2); break; }
+    constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, C::kAmn, C::kBmn);
+    int s = 0;
+    uint32_t ph = 0;
+    int64_t local = 0;
+    bool issued = false, ok = true;
+    for (int64_t tile = blockIdx.x; tile < tiles && ok && !warp_abort(); tile += gridDim.x, ++local) {
+      const int buf = static_cast<int>(local & 1);
+      const uint32_t use = static_cast<uint32_t>(local >> 1);
+      if (!__all_sync(0xffffffffu, mbar_wait(&tempty[buf], (use & 1) ^ 1, lim))) {
+        fail(p, abort_flag, 2);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t dt = tmem + buf * BN;
+      for (int64_t kb = 0; kb < kblocks; ++kb) {
+        uint64_t* ready = (DW > 0) ? &decd[s] : &full[s];
+        if (!__all_sync(0xffffffffu, mbar_wait(ready, ph, lim))) {
+          fail(p, abort_flag, 3);
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const uint32_t dt = tmem + buf * BN;
-        bool ok = true;
-        for (int64_t kb = 0; kb < kblocks; ++kb) {
-          uint64_t* ready = (DW > 0) ? &decd[s] : &full[s];
-          if (!mbar_wait(ready, ph, lim)) { fail(p, abort_flag, 3); ok = false; break; }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + s * A_BYTES);
-          const uint32_t b0 = smem_u32(sB + s * B_BYTES);
+        const uint32_t a0 = smem_u32(sA + s * A_BYTES);
+        const uint32_t b0 = smem_u32(sB + s * B_BYTES);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k) {
             const uint64_t ad = C::kAmn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
@@ -371,19 +384,22 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
                                         : sdesc_sw128(b0 + k * 32, 16, 1024);
             mma_ss(dt, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);
           }
-          issued = true;
           mma_commit(&empty[s]);
-          if (++s == STAGES) { s = 0; ph ^= 1; }
         }
-        if (!ok) break;
-        mma_commit(&tfull[buf]);
+        __syncwarp();
+        issued = true;
+        if (++s == STAGES) { s = 0; ph ^= 1; }
       }
-      if (issued) {  // no MMA may still run when TMEM is released
-        mma_commit(drain);
-        // the default limit: running MMAs finish in microseconds, and TMEM may
-        // be released only after them
-        if (!mbar_wait(drain, 0, kDefaultWaitLimit)) fail(p, abort_flag, 4);
-      }
+      if (!ok) break;
+      if (elect_one()) mma_commit(&tfull[buf]);
+      __syncwarp();
+    }
+    if (issued) {  // no MMA may still run when TMEM is released
+      if (elect_one()) mma_commit(drain);
+      __syncwarp();
+      // the default limit: running MMAs finish in microseconds, and TMEM may
+      // be released only after them
+      if (!mbar_wait(drain, 0, kDefaultWaitLimit)) fail(p, abort_flag, 4);
     }
   } else if (warp < 2 + DW) {
     // ------------------------------------------------------------ decoders
@@ -623,23 +639,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      int64_t issued = 0;
-      for (int64_t tile = pair; tile < tiles && !*abort_flag; tile += npairs) {
-        int mt, nt;
-        tile_coords(tile, m_tiles, n_tiles, kBand, mt, nt);
-        const int row0 = mt * 2 * BM + static_cast<int>(rank) * BM;  // this CTA's A rows
-        const int col0 = nt * BN + static_cast<int>(rank) * (BN / 2);  // this CTA's B rows
-        for (int64_t kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1, lim)) { fail(p, abort_flag, 11); break; }
-          if (*abort_flag) break;
-          ++issued;
-          uint8_t* st = smem + size_t(s) * C::kStage;
-          const uint32_t fa0 = mapa_shared(smem_u32(&fullA[s]), 0);
+    // (the whole warp runs the loop; an elected lane issues, see elect_one)
+    const uint32_t bar0 = mapa_shared(smem_u32(fullA), 0);
+    int s = 0;
+    uint32_t ph = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t tile = pair; tile < tiles && ok; tile += npairs) {
+      int mt, nt;
+      tile_coords(tile, m_tiles, n_tiles, kBand, mt, nt);
+      const int row0 = mt * 2 * BM + static_cast<int>(rank) * BM;  // this CTA's A rows
+      const int col0 = nt * BN + static_cast<int>(rank) * (BN / 2);  // this CTA's B rows
+      for (int64_t kb = 0; kb < kblocks; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1, lim))) {
+          fail(p, abort_flag, 11);
+          ok = false;
+          break;
+        }
+        if (warp_abort()) { ok = false; break; }
+        ++issued;
+        uint8_t* st = smem + size_t(s) * C::kStage;
+        const uint32_t fa0 = bar0 + 8 * s;
+        const int kx = static_cast<int>(kb);
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&fullA[s], 2 * C::kOperandTx);
-          const int kx = static_cast<int>(kb);
           if constexpr (KIND == kFwdAlg || KIND == kFwdDec) {
             mbar_arrive_expect_tx(&fullC[s], C::kC);
             tma_load_2d(&tmB, &fullC[s], st + C::kA + C::kB, kx * (BK / 4), col0);
@@ -654,45 +677,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
             tma_load_2d_pair(&tmB, fa0, st + C::kA, col0, kx * BK);
             tma_load_2d_pair(&tmB, fa0, st + C::kA + 8192, col0 + 64, kx * BK);
           }
-          if (++s == S) { s = 0; ph ^= 1; }
         }
+        __syncwarp();
+        if (++s == S) { s = 0; ph ^= 1; }
       }
-      if (*abort_flag) {
-        // wait for this CTA's own copies in flight (codes, on its own barrier);
-        // the even CTA also waits for the operand stages, which count both
-        // CTAs' bytes.  The default limit: copies in flight finish quickly.
-        for (int64_t n = issued - 1; n >= 0 && n >= issued - S; --n) {
-          const uint32_t par = static_cast<uint32_t>((n / S) & 1);
-          if (C::kHasCodes) mbar_wait(&fullC[n % S], par, kDefaultWaitLimit);
-          if (rank == 0) mbar_wait(&fullA[n % S], par, kDefaultWaitLimit);
-        }
+    }
+    if (warp_abort()) {
+      // wait for this CTA's own copies in flight (codes, on its own barrier);
+      // the even CTA also waits for the operand stages, which count both
+      // CTAs' bytes.  The default limit: copies in flight finish quickly.
+      for (int64_t n = issued - 1; n >= 0 && n >= issued - S; --n) {
+        const uint32_t par = static_cast<uint32_t>((n / S) & 1);
+        if (C::kHasCodes) mbar_wait(&fullC[n % S], par, kDefaultWaitLimit);
+        if (rank == 0) mbar_wait(&fullA[n % S], par, kDefaultWaitLimit);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, BN, C::kAmn, C::kBmn);
       int s = 0;
       uint32_t ph = 0;
       int64_t local = 0, it = 0;
-      bool issued = false;
-      for (int64_t tile = pair; tile < tiles && !*abort_flag; tile += npairs, ++local) {
+      bool issued = false, ok = true;
+      for (int64_t tile = pair; tile < tiles && ok && !warp_abort(); tile += npairs, ++local) {
         const int buf = static_cast<int>(local & 1);
         const uint32_t use = static_cast<uint32_t>(local >> 1);
         // the odd CTA's epilogue arrives from the other SM: acquire at cluster scope
-        if (!mbar_wait_cluster(&tempty[buf], (use & 1) ^ 1, lim)) { fail(p, abort_flag, 12); break; }
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[buf], (use & 1) ^ 1, lim))) {
+          fail(p, abort_flag, 12);
+          break;
+        }
         tc_fence_after();
         const uint32_t dt = tmem + buf * BN;
-        bool ok = true;
         for (int64_t kb = 0; kb < kblocks; ++kb, ++it) {
-          if (!mbar_wait(&fullA[s], ph, lim)) { fail(p, abort_flag, 13); ok = false; break; }
+          if (!__all_sync(0xffffffffu, mbar_wait(&fullA[s], ph, lim))) {
+            fail(p, abort_flag, 13);
+            ok = false;
+            break;
+          }
           if constexpr (C::kHasCodes) {
-            if (!mbar_wait(&decd[s], ph, lim)) { fail(p, abort_flag, 14); ok = false; break; }
+            if (!__all_sync(0xffffffffu, mbar_wait(&decd[s], ph, lim))) {
+              fail(p, abort_flag, 14);
+              ok = false;
+              break;
+            }
             // the odd CTA's half of B: one cluster-scope wait per group of k blocks
             const int64_t q = it / kPeerGroup;
             if (it % kPeerGroup == 0 &&
-                !mbar_wait_cluster(&decd_peer[q % S], static_cast<uint32_t>((q / S) & 1),
-                                   lim)) {
+                !__all_sync(0xffffffffu, mbar_wait_cluster(&decd_peer[q % S],
+                                                           static_cast<uint32_t>((q / S) & 1), lim))) {
               fail(p, abort_flag, 18);
               ok = false;
               break;
@@ -701,23 +735,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
           tc_fence_after();
           const uint32_t a0 = smem_u32(smem + size_t(s) * C::kStage);
           const uint32_t b0 = a0 + C::kA;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) {
-            const uint64_t ad = C::kAmn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
-                                        : sdesc_sw128(a0 + k * 32, 16, 1024);
-            const uint64_t bd = C::kBmn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
-                                        : sdesc_sw128(b0 + k * 32, 16, 1024);
-            mma_ss_pair(dt, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint64_t ad = C::kAmn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
+                                          : sdesc_sw128(a0 + k * 32, 16, 1024);
+              const uint64_t bd = C::kBmn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
+                                          : sdesc_sw128(b0 + k * 32, 16, 1024);
+              mma_ss_pair(dt, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+            }
+            mma_commit_pair(&empty[s]);
           }
+          __syncwarp();
           issued = true;
-          mma_commit_pair(&empty[s]);
           if (++s == S) { s = 0; ph ^= 1; }
         }
         if (!ok) break;
-        mma_commit_pair(&tfull[buf]);
+        if (elect_one()) mma_commit_pair(&tfull[buf]);
+        __syncwarp();
       }
       if (issued) {
-        mma_commit_pair(drain);
+        if (elect_one()) mma_commit_pair(drain);
+        __syncwarp();
         // the default limit: TMEM may be released only after the running MMAs
         if (!mbar_wait(drain, 0, kDefaultWaitLimit)) fail(p, abort_flag, 15);
       }
