@@ -74,6 +74,7 @@ lcvq_status check_device() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 constexpr int64_t kMaxGemmDim = int64_t(1) << 30;
 constexpr int64_t kMaxLdlqDim = int64_t(1) << 20;  // U is d_in^2 floats
 constexpr int64_t kMaxFitHDin = int64_t(1) << 16;  // the Gram is ~12 d_in^2 bytes
@@ -612,16 +613,29 @@ lcvq_status lcvq_gemm_ckpt(const void* X, lcvq_dtype dtype, int64_t M, const uin
     if (!aligned16(X) || !aligned16(X8) || !aligned16(S8)) return LCVQ_ERR_ALIGNMENT;
     if (d_out > 0) {  // everything lcvq_gemm would refuse, before the first launch
       if (!Y || !packed || !A || !B || !workspace) return LCVQ_ERR_INVALID_ARG;
-      if (!aligned16(Y) || !aligned16(packed) || !aligned16(A) || !aligned16(B) || !aligned16(workspace))
+      if (!aligned16(Y) || !aligned16(packed) || !aligned16(A) || !aligned16(B) || !aligned256(workspace))
         return LCVQ_ERR_ALIGNMENT;
       if (ws_bytes < gemm_ws(dtype, M, d_in).total) return LCVQ_ERR_WORKSPACE;
     }
     if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
   }
   int launches = 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (keep && d_out > 0 && dtype == LCVQ_BF16 && M > 32) {
+    // one pass over X for the transform and the packing, then the integer-code GEMM
+    const GemmWs w = gemm_ws(dtype, M, d_in);
+    char* ws = static_cast<char*>(workspace);
+    uint16_t* Xpp = reinterpret_cast<uint16_t*>(ws + w.xpp_off);
+    float* corr = reinterpret_cast<float*>(ws + w.corr_off);
+    cudaError_t e = launch_xform_ckpt(static_cast<const uint16_t*>(X), M, d_in, d, A, B, Xpp, corr, X8,
+                                      S8, s, &launches);
+    if (e == cudaSuccess)
+      e = launch_tc_forward_int(Xpp, corr, M, packed, d_out, d_in, static_cast<uint16_t*>(Y),
+                                reinterpret_cast<unsigned int*>(ws), s, &launches);
+    return finish(e, launches);
+  }
   if (keep) {
-    cudaError_t e = launch_mx_pack(X, dtype == LCVQ_F32, M, d_in, d_in, false, X8, S8,
-                                   static_cast<cudaStream_t>(stream), &launches);
+    cudaError_t e = launch_mx_pack(X, dtype == LCVQ_F32, M, d_in, d_in, false, X8, S8, s, &launches);
     if (e != cudaSuccess) return LCVQ_ERR_CUDA;
   }
   lcvq_status st = lcvq_gemm(X, dtype, M, packed, d_out, d_in, d, A, B, Y, LCVQ_FORM_AUTO, workspace,
@@ -647,7 +661,7 @@ lcvq_status lcvq_gemm_backward_ckpt(const uint8_t* X8, const uint8_t* S8, const 
   if (!X8 || !S8 || !dY || !packed || !A || !B || !workspace) return LCVQ_ERR_INVALID_ARG;
   if (!aligned16(dA) || !aligned16(dB) || (dWp && !aligned16(dWp)) || (dX && !aligned16(dX)) ||
       (mask_bits && !aligned16(mask_bits)) || !aligned16(X8) || !aligned16(S8) || !aligned16(dY) ||
-      !aligned16(packed) || !aligned16(A) || !aligned16(B) || !aligned16(workspace))
+      !aligned16(packed) || !aligned16(A) || !aligned16(B) || !aligned256(workspace))
     return LCVQ_ERR_ALIGNMENT;
   if (ws_bytes < bwd_ckpt_ws(dtype, M, d_out, d_in, d)) return LCVQ_ERR_WORKSPACE;
   if (lcvq_status st = check_device(); st != LCVQ_OK) return st;

@@ -1,0 +1,153 @@
+// The X-transform of a training forward that keeps X in 8 bits: one pass over X
+// writes X'' (see xform.cu for the algebra and the order), the per-row constant of
+// the integer-code GEMM, and X packed into mx8 (see mx.cuh).
+//
+// For codes that enter as 4^p z (no 128 offset, tc_gemm.cu kind FwdInt)
+//     Y[m][n] = sum_k X''_k 4^p z_k + corr,  corr = s' - 3/2 sum_k bf16(X')_k,
+// s' = sum_g x_g^T (B + 3/2 A 1): the centred algebraic form.
+//
+// Bound by HBM: 2 B an element read, 3.03 written (3.03 read and 5.03 written by
+// the X-transform and the packing one after the other).  A CTA takes whole rows in
+// turn with A in registers; a thread transforms a block of 16 elements (two
+// 16-byte loads, one 32-byte store of X'', one 16-byte store of codes), two threads
+// share a scale.  The sums of a row go into fp64 per 16-block and through one
+// warp tree and an ordered sum over the warps.
+#include "common.cuh"
+#include "gemv_common.cuh"
+#include "internal.h"
+#include "mx_pack.cuh"
+#include "xform.cuh"
+
+namespace lcvq {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 2;  // blocks whose loads a thread has in flight
+
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    xform_ckpt_kernel(const uint16_t* X, int64_t M, int64_t d_in, const float* A, const float* B,
+                      uint16_t* __restrict__ Xpp, float* __restrict__ corr, uint8_t* __restrict__ X8,
+                      uint8_t* __restrict__ S8) {
+  __shared__ float sA[D * D], sB[D], sBp[D];
+  __shared__ double red[2][kThreads / 32];
+  griddep_wait();  // X, A and B may come from the kernel just before this one
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < D * D) sA[threadIdx.x] = ld_global_f32(A + threadIdx.x);
+  if (threadIdx.x < D) sB[threadIdx.x] = ld_global_f32(B + threadIdx.x);
+  __syncthreads();
+  if (threadIdx.x < D) sBp[threadIdx.x] = shifted_offset<D>(sA + threadIdx.x * D, sB[threadIdx.x]);
+  __syncthreads();
+  float rA[D * D], rBp[D];
+#pragma unroll
+  for (int i = 0; i < D * D; ++i) rA[i] = sA[i];
+#pragma unroll
+  for (int i = 0; i < D; ++i) rBp[i] = sBp[i];
+
+  const int64_t blocks = d_in / 16, tiles_k = mx::scale_tiles_k(d_in);
+  for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+    const uint16_t* xr = X + m * d_in;
+    double s_b = 0.0, s_xr = 0.0;
+    for (int64_t b0 = threadIdx.x; b0 - threadIdx.x < blocks; b0 += kAhead * kThreads) {
+      uint4 u[kAhead][2];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t b = b0 + i * kThreads;
+        u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
+        if (b < blocks) {
+          u[i][0] = ld_global_v4(xr + 16 * b);
+          u[i][1] = ld_global_v4(xr + 16 * b + 8);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t b = b0 + i * kThreads;
+        // mx8: two neighbouring lanes hold a block of 32 (d_in is a multiple of 64,
+        // so both are inside the row or outside)
+        mx::Eight<false> e[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          e[h].w[0] = u[i][h].x; e[h].w[1] = u[i][h].y; e[h].w[2] = u[i][h].z; e[h].w[3] = u[i][h].w;
+        }
+        uint32_t mb = max(e[0].max_bits(), e[1].max_bits());
+        mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+        if (b >= blocks) {
+          // the tile's columns beyond the last (half a tile: d_in is a multiple of 64)
+          if (b < tiles_k * 8 && (lane & 1) == 0)
+            S8[mx::scale_word(m, b >> 3, tiles_k) + ((b >> 1) & 3)] = 0;
+          continue;
+        }
+        const uint32_t sb = mx::scale_byte<false>(mb);
+        const uint2 q0 = mx::pack8<false, false>(e[0], sb), q1 = mx::pack8<false, false>(e[1], sb);
+        *reinterpret_cast<uint4*>(X8 + m * d_in + 16 * b) = make_uint4(q0.x, q0.y, q1.x, q1.y);
+        if ((lane & 1) == 0) S8[mx::scale_word(m, b >> 3, tiles_k) + ((b >> 1) & 3)] = sb;
+
+        uint32_t o[8];
+        float fb, fxr, fxpp;
+        xform_block<D>(u[i][0], u[i][1], rA, rBp, o, fb, fxr, fxpp);
+        st_global_32(Xpp + m * d_in + 16 * b, o);
+        s_b += double(fb);
+        s_xr += double(fxr);
+      }
+    }
+    s_b = chunk_tree_sum(s_b);
+    s_xr = chunk_tree_sum(s_xr);
+    if (lane == 0) {
+      red[0][warp] = s_b;
+      red[1][warp] = s_xr;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double a = 0.0, r = 0.0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        a += red[0][w];
+        r += red[1][w];
+      }
+      corr[m] = static_cast<float>(a - 1.5 * r);
+    }
+    __syncthreads();
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const uint16_t* X, int64_t M, int64_t d_in, const float* A, const float* B,
+                     uint16_t* Xpp, float* corr, uint8_t* X8, uint8_t* S8, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  const int64_t most = int64_t(kNumSMsB200) * 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(M < most ? M : most), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaError_t e = cudaLaunchKernelEx(&cfg, xform_ckpt_kernel<D>, X, M, d_in, A, B, Xpp, corr, X8, S8);
+      e != cudaSuccess)
+    return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_xform_ckpt(const uint16_t* X, int64_t M, int64_t d_in, int d, const float* A,
+                              const float* B, uint16_t* Xpp, float* corr, uint8_t* X8, uint8_t* S8,
+                              cudaStream_t s, int* launches) {
+  ++*launches;
+  switch (d) {
+    case 1: return launch_d<1>(X, M, d_in, A, B, Xpp, corr, X8, S8, s);
+    case 2: return launch_d<2>(X, M, d_in, A, B, Xpp, corr, X8, S8, s);
+    case 4: return launch_d<4>(X, M, d_in, A, B, Xpp, corr, X8, S8, s);
+    default: return launch_d<8>(X, M, d_in, A, B, Xpp, corr, X8, S8, s);
+  }
+}
+
+}  // namespace lcvq

@@ -45,6 +45,12 @@ cudaError_t launch_xform_i8(const uint16_t* X, int64_t M, int64_t d_in, int d, c
                             const float* B, uint8_t* X8, float* corr, float* inv_s, cudaStream_t s,
                             int* launches);
 
+// X'' as launch_xform forms it and X packed into mx8, in one pass over X;
+// corr[M] = s' - 3/2 sum_k bf16(X')[m][k]
+cudaError_t launch_xform_ckpt(const uint16_t* X, int64_t M, int64_t d_in, int d, const float* A,
+                              const float* B, uint16_t* Xpp, float* corr, uint8_t* X8, uint8_t* S8,
+                              cudaStream_t s, int* launches);
+
 // ---- decode-GEMV (bf16, M <= 32) ----
 // after_xform: launched right after launch_xform of the same call on the same
 // stream, so the codes may be read before the kernel's dependency wait.
@@ -151,6 +157,11 @@ cudaError_t launch_tc_forward(const uint16_t* Xa, bool algebraic, const float* c
                               const uint8_t* packed, int64_t d_out, int64_t d_in, int d,
                               const float* A, const float* B, uint16_t* Y, unsigned int* err,
                               cudaStream_t s, int* launches);
+// the algebraic form without the 128 offset: Y = sum_k X''[m][k] 4^p z[n][k] + corr[m],
+// corr as launch_xform_ckpt writes it
+cudaError_t launch_tc_forward_int(const uint16_t* Xpp, const float* corr, int64_t M,
+                                  const uint8_t* packed, int64_t d_out, int64_t d_in, uint16_t* Y,
+                                  unsigned int* err, cudaStream_t s, int* launches);
 cudaError_t launch_tc_backward_dx(const uint16_t* dY, const float* rsum, int64_t M,
                                   const uint8_t* packed, int64_t d_out, int64_t d_in, int d,
                                   const float* A, const float* B, uint16_t* dX, unsigned int* err,

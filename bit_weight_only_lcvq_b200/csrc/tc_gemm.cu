@@ -17,6 +17,11 @@
 // Kinds (D[i][j] = sum_c A[i][c] B[j][c]):
 //   FwdAlg  Y[m][n]  = sum_k X''[m][k] v[n][k] + corr[m]      A = X'' (K-major)
 //           v = 128 + 4^p z: one LOP3 per bf16 pair (see xform.cu)
+//   FwdInt  the same with v = 4^p z: 128 is subtracted from the decoded pairs (one
+//           more instruction each), so that the fp32 sums stay near Y's own size.
+//           With 128 in every term they run 60 times as high, and over a long K the
+//           additions, which the tensor core truncates, show in Y: 2.6e-3 of its
+//           norm against 2.35e-3 at K = 14336 (X' and Y rounded to bf16 make 2.35e-3)
 //   FwdDec  Y[m][n]  = sum_k X[m][k] bf16(A z + B)[n][k]      A = X (K-major)
 //           decoders evaluate A z + B in fp32 (LC-QAT Methodology 1, c = A z + B)
 //   Dx      P[m][k]  = sum_n dY[m][n] v[n][k]                 A = dY (K-major),
@@ -60,7 +65,8 @@ constexpr int C_BYTES = 4096;         // packed codes of one stage
 constexpr int kPairPeerGroup = 3;
 constexpr int kTmemCols = 512;
 
-enum Kind { kFwdAlg = 0, kFwdDec = 1, kDx = 2, kDw = 3, kGram = 4 };
+enum Kind { kFwdAlg = 0, kFwdDec = 1, kDx = 2, kDw = 3, kGram = 4, kFwdInt = 5 };
+constexpr bool is_alg(int kind) { return kind == kFwdAlg || kind == kFwdInt; }
 
 struct Params {
   int64_t M, N, K;    // D is M x N, contraction K (see each kind)
@@ -79,6 +85,10 @@ struct Params {
 template <int KIND, int DW>
 struct Cfg {
   static constexpr int kThreads = 32 * (2 + DW + 4);
+  // groups of four decoder warps take alternate k blocks: a group's chain from the
+  // codes' arrival to the decoded tile is longer than the MMAs of a k block
+  static constexpr int kDecGroups = DW < 8 ? 1 : DW / 4;
+  static constexpr int kGroupWarps = DW > 0 ? DW / kDecGroups : 1;
   static constexpr bool kHasCodes = KIND != kDw && KIND != kGram;
   static constexpr bool kAmn = KIND == kDw || KIND == kGram;
   static constexpr bool kBmn = KIND == kDx || KIND == kDw || KIND == kGram;
@@ -116,6 +126,16 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
+// bf16 pairs less 128, exact on the code decoder's 128 + 4^p z
+__device__ __forceinline__ uint4 minus_128(const uint4& v) {
+  auto sub = [](uint32_t a) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(0x43004300u));
+    return r;
+  };
+  return make_uint4(sub(v.x), sub(v.y), sub(v.z), sub(v.w));
+}
+
 // One 32-column chunk of a D row (registers r[] from TMEM): the fused
 // epilogue of each kind.  gm is the D row, gn0 the first D column.
 template <int KIND, int D>
@@ -123,7 +143,7 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const float* sAm
                                                const uint32_t (&r)[32], int64_t gm, int64_t gn0,
                                                float addc, float rs, float (&pa)[D * D],
                                                float (&pb)[D]) {
-  if constexpr (KIND == kFwdAlg || KIND == kFwdDec) {
+  if constexpr (is_alg(KIND) || KIND == kFwdDec) {
     uint16_t* Y = static_cast<uint16_t*>(p.out) + gm * p.N + gn0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -272,7 +292,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&decd[s], DW > 0 ? DW : 1);     // one arrive per decoder warp
+      mbar_init(&decd[s], C::kGroupWarps);      // one arrive per decoder warp of the stage's group
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -283,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if constexpr (KIND != kFwdAlg && KIND != kGram) {  // these never touch A, B
+  if constexpr (!is_alg(KIND) && KIND != kGram) {  // these never touch A, B
     if (threadIdx.x < D * D) sAm[threadIdx.x] = p.Amat[threadIdx.x];
     if (KIND != kDw && threadIdx.x >= 64 && threadIdx.x < 64 + D)
       sAm[D * D + threadIdx.x - 64] = p.Bvec[threadIdx.x - 64];
@@ -326,7 +346,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
         const int kx = static_cast<int>(kb);
         if (elect_one()) {
           mbar_arrive_expect_tx(&full[s], C::kStageTx);
-          if constexpr (KIND == kFwdAlg || KIND == kFwdDec) {
+          if constexpr (is_alg(KIND) || KIND == kFwdDec) {
             tma_load_2d(&tmA, &full[s], sA + s * A_BYTES, kx * BK, mt * BM);
             tma_load_2d(&tmB, &full[s], sC + s * C_BYTES, kx * (BK / 4), nt * BN);
           } else if constexpr (KIND == kDx) {
@@ -403,21 +423,29 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
     }
   } else if (warp < 2 + DW) {
     // ------------------------------------------------------------ decoders
-    const int dt = threadIdx.x - 64;  // 0 .. 32*DW-1
-    int s = 0;
+    constexpr int GW = C::kGroupWarps;
+    const int grp = (warp - 2) / GW;
+    const int dt = (threadIdx.x - 64) % (32 * GW);
+    int s = 0, turn = 0;  // turn: the group that owns the next k block
     uint32_t ph = 0;
     for (int64_t tile = blockIdx.x; tile < tiles && !warp_abort(); tile += gridDim.x) {
       for (int64_t kb = 0; kb < kblocks; ++kb) {
+        const bool mine = turn == grp;
+        if (++turn == C::kDecGroups) turn = 0;
+        if (!mine) {
+          if (++s == STAGES) { s = 0; ph ^= 1; }
+          continue;
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, lim))) {  // one outcome per warp
           fail(p, abort_flag, 5);
           break;
         }
         const uint8_t* cs = sC + s * C_BYTES;
         const uint32_t bs = smem_u32(sB + s * B_BYTES);
-        if constexpr (KIND == kFwdAlg) {
+        if constexpr (is_alg(KIND)) {
 #pragma unroll
-          for (int rr = 0; rr < BN / (32 * DW); ++rr) {
-            const int r = dt + rr * 32 * DW;
+          for (int rr = 0; rr < BN / (32 * GW); ++rr) {
+            const int r = dt + rr * 32 * GW;
             const uint4 cw = *reinterpret_cast<const uint4*>(cs + r * 16);
             const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
             const uint32_t row = bs + r * 128;
@@ -425,14 +453,18 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
             for (int q = 0; q < 4; ++q) {
               uint4 c0, c1;
               dec_word(w[q], c0, c1);
+              if constexpr (KIND == kFwdInt) {
+                c0 = minus_128(c0);
+                c1 = minus_128(c1);
+              }
               st_shared_v4(row + (((2 * q) ^ (r & 7)) << 4), c0);
               st_shared_v4(row + (((2 * q + 1) ^ (r & 7)) << 4), c1);
             }
           }
         } else if constexpr (KIND == kFwdDec) {
 #pragma unroll
-          for (int rr = 0; rr < BN / (32 * DW); ++rr) {
-            const int r = dt + rr * 32 * DW;
+          for (int rr = 0; rr < BN / (32 * GW); ++rr) {
+            const int r = dt + rr * 32 * GW;
             const uint4 cw = *reinterpret_cast<const uint4*>(cs + r * 16);
             const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
             const uint32_t row = bs + r * 128;
@@ -464,8 +496,8 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
           // codes tile [64 contraction rows n][64 B = 256 output k]; B tile is
           // MN-major: 4 blocks of 64 k (8 KB), each [64 n lines][128 B]
 #pragma unroll
-          for (int it = 0; it < (64 * 4) / (32 * DW); ++it) {
-            const int u = dt + it * 32 * DW;  // (row n_l, block q): a warp = 32 rows of one block
+          for (int it = 0; it < (64 * 4) / (32 * GW); ++it) {
+            const int u = dt + it * 32 * GW;  // (row n_l, block q): a warp = 32 rows of one block
             const int nl = u & 63, q = u >> 6;
             const uint4 cw = *reinterpret_cast<const uint4*>(cs + nl * 64 + q * 16);
             const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
@@ -510,7 +542,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
       const int64_t gm = int64_t(mt) * BM + row;  // D row
       const uint32_t tbase = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
       float addc = 0.f;
-      if constexpr (KIND == kFwdAlg) addc = gm < p.M ? p.corr[gm] : 0.f;
+      if constexpr (is_alg(KIND)) addc = gm < p.M ? p.corr[gm] : 0.f;
       float rs = 0.f;
       if constexpr (KIND == kDx) rs = gm < p.M ? p.rsum[gm] : 0.f;
 #pragma unroll 1
@@ -942,6 +974,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
 }
 
 // ---------------------------------------------------------------- host side
+// decoder warps of the single-CTA kinds (8192 x 14336 -> 4096): dX with one group of
+// four 860 us, with two 790, with three 795; the forward, whose main loop the
+// power limit paces, 770 with one, two or three
+constexpr int kAlgDecWarps = 4, kDxDecWarps = 8;
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -1066,8 +1103,23 @@ cudaError_t launch_tc_forward(const uint16_t* Xa, bool algebraic, const float* c
   Params p{};
   p.M = M; p.N = d_out; p.K = d_in; p.d_in = d_in; p.d_out = d_out;
   p.codes = packed; p.corr = corr; p.Amat = A; p.Bvec = B; p.out = Y; p.err = err;
-  cudaError_t e = algebraic ? launch_kind<kFwdAlg, 8, 4>(ta, tb, p, s, nullptr)
+  cudaError_t e = algebraic ? launch_kind<kFwdAlg, 8, kAlgDecWarps>(ta, tb, p, s, nullptr)
                             : launch_kind2_d<kFwdDec, 8>(d, ta, tb, p, s, nullptr);
+  ++*launches;
+  return e;
+}
+
+cudaError_t launch_tc_forward_int(const uint16_t* Xpp, const float* corr, int64_t M,
+                                  const uint8_t* packed, int64_t d_out, int64_t d_in, uint16_t* Y,
+                                  unsigned int* err, cudaStream_t s, int* launches) {
+  CUtensorMap ta, tb;
+  if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Xpp, d_in, M, d_in * 2, BK, BM, true) ||
+      !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, packed, d_in / 4, d_out, d_in / 4, BK / 4, BN, false))
+    return cudaErrorInvalidValue;
+  Params p{};
+  p.M = M; p.N = d_out; p.K = d_in; p.d_in = d_in; p.d_out = d_out;
+  p.codes = packed; p.corr = corr; p.out = Y; p.err = err;
+  cudaError_t e = launch_kind<kFwdInt, 8, kAlgDecWarps>(ta, tb, p, s, nullptr);
   ++*launches;
   return e;
 }
@@ -1084,7 +1136,7 @@ cudaError_t launch_tc_backward_dx(const uint16_t* dY, const float* rsum, int64_t
   Params p{};
   p.M = M; p.N = d_in; p.K = d_out; p.d_in = d_in; p.d_out = d_out;
   p.codes = packed; p.rsum = rsum; p.Amat = A; p.Bvec = B; p.out = dX; p.err = err;
-  cudaError_t e = launch_kind_d<kDx, 4>(d, ta, tb, p, s, nullptr);
+  cudaError_t e = launch_kind_d<kDx, kDxDecWarps>(d, ta, tb, p, s, nullptr);
   ++*launches;
   return e;
 }

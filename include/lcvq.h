@@ -440,12 +440,16 @@ LCVQ_API lcvq_status lcvq_mx4_gemm(const uint8_t* X4, const uint8_t* SX, int64_t
                                    int64_t d_in, void* Y, lcvq_dtype y_dtype, void* workspace,
                                    size_t ws_bytes, void* stream);
 
-/* A training forward that keeps X at half its bytes: Y = X W~ exactly as
- * lcvq_gemm computes it (form AUTO), and X packed into MX8 exactly as
- * lcvq_mx_pack packs it (ld = d_in), for lcvq_gemm_backward_ckpt.
+/* A training forward that keeps X at half its bytes: Y = X W~, and X packed into
+ * MX8 exactly as lcvq_mx_pack packs it (ld = d_in), for lcvq_gemm_backward_ckpt.
+ * For bf16 and M > 32 one pass over X forms X'' (as lcvq_xform) and packs X, and
+ * the codes enter the GEMM as 4^p z instead of 128 + 4^p z: Y is the algebraic
+ * form's to within the rounding of its fp32 sums, not bit for bit.  Otherwise Y has
+ * lcvq_gemm's bits (form AUTO).
  *   X8 [M][d_in] and S8 (lcvq_mx_scale_bytes(M, d_in) bytes) out; the rest as
  *   lcvq_gemm.
- *   workspace: >= lcvq_workspace_size(LCVQ_OP_GEMM_CKPT, dtype, M, d_out, d_in, d).
+ *   workspace: >= lcvq_workspace_size(LCVQ_OP_GEMM_CKPT, dtype, M, d_out, d_in, d)
+ *   bytes, 256-byte aligned (LCVQ_ERR_ALIGNMENT), first 256 bytes zeroed once.
  * Shapes as lcvq_gemm.  M == 0 or d_in == 0 keeps nothing; d_out == 0 keeps X. */
 LCVQ_API lcvq_status lcvq_gemm_ckpt(const void* X, lcvq_dtype dtype, int64_t M,
                                     const uint8_t* packed, int64_t d_out, int64_t d_in, int d,
