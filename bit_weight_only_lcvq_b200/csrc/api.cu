@@ -630,7 +630,7 @@ lcvq_status lcvq_gemm_ckpt(const void* X, lcvq_dtype dtype, int64_t M, const uin
     cudaError_t e = launch_xform_ckpt(static_cast<const uint16_t*>(X), M, d_in, d, A, B, Xpp, corr, X8,
                                       S8, s, &launches);
     if (e == cudaSuccess)
-      e = launch_tc_forward_int(Xpp, corr, M, packed, d_out, d_in, static_cast<uint16_t*>(Y),
+      e = launch_tc_forward_top(Xpp, corr, M, packed, d_out, d_in, static_cast<uint16_t*>(Y),
                                 reinterpret_cast<unsigned int*>(ws), s, &launches);
     return finish(e, launches);
   }

@@ -1,14 +1,16 @@
 // The X-transform of a training forward that keeps X in 8 bits: one pass over X
-// writes X'' (see xform.cu for the algebra and the order), the per-row constant of
-// the integer-code GEMM, and X packed into mx8 (see mx.cuh).
+// writes X'' in the decoder's order (see xform.cu), the per-row constant of the
+// integer-code GEMM, and X packed into mx8 (see mx.cuh).
 //
-// For codes that enter as 4^p z (no 128 offset, tc_gemm.cu kind FwdInt)
-//     Y[m][n] = sum_k X''_k 4^p z_k + corr,  corr = s' - 3/2 sum_k bf16(X')_k,
+// The codes enter the GEMM as 128 + 32 z (tc_gemm.cu kind FwdTop), so with
+// X'r = bf16(X') and X'' = X'r / 32
+//     sum_k X''_k (128 + 32 z_k) = sum_k X'r_k z_k + 4 sum_k X'r_k,
+//     Y[m][n] = that + corr,  corr = s' - (3/2 + 4) sum_k X'r_k,
 // s' = sum_g x_g^T (B + 3/2 A 1): the centred algebraic form.
 //
 // Bound by HBM: 2 B an element read, 3.03 written (3.03 read and 5.03 written by
 // the X-transform and the packing one after the other).  A CTA takes whole rows in
-// turn with A in registers; a thread transforms a block of 16 elements (two
+// turn (A in shared memory, read by all lanes at once); a thread transforms a block of 16 elements (two
 // 16-byte loads, one 32-byte store of X'', one 16-byte store of codes), two threads
 // share a scale.  The sums of a row go into fp64 per 16-block and through one
 // warp tree and an ordered sum over the warps.
@@ -31,12 +33,78 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
+// two fp32 multiply-adds in one instruction
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};\n" : "=l"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
+// X'' of one 16-element block and its parts of corr, on paired multiply-adds.  sAs
+// is A / 32, a power of two, so rounding commutes with it.
+//   o[c] = bf16x2 of positions c and c + 8;  sb = sum x B';  sxr = 32 sum X''
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__device__ __forceinline__ void top_block(const uint4& u0, const uint4& u1, const float* sAs,
+                                          const float* sBp, uint32_t (&o)[8], float& sb, float& sxr) {
+  const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+  auto x = [&](int k) { return k & 1 ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1]); };
+  float xp[16];
+  if constexpr (D == 1) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) xp[k] = x(k) * sAs[0];
+  } else {
+    constexpr int kV = 16 / D, kJ = D / 2;  // vectors, pairs of columns
+    uint64_t acc[kV][kJ] = {};
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      uint64_t a[kJ];
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) a[j] = *reinterpret_cast<const uint64_t*>(sAs + D * i + 2 * j);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        const uint64_t xx = twice(x(D * v + i));
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) acc[v][j] = fma2(xx, a[j], acc[v][j]);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const float2 f = halves(acc[v][j]);
+        xp[D * v + 2 * j] = f.x;
+        xp[D * v + 2 * j + 1] = f.y;
+      }
+  }
+  sb = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) sb = fmaf(x(k), sBp[k % D], sb);
+  sxr = 0.f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    o[c] = pack_bf16x2(xp[c], xp[c + 8]);
+    sxr += bf16_lo(o[c]) + bf16_hi(o[c]);
+  }
+  sxr *= 32.f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 4)
     xform_ckpt_kernel(const uint16_t* X, int64_t M, int64_t d_in, const float* A, const float* B,
                       uint16_t* __restrict__ Xpp, float* __restrict__ corr, uint8_t* __restrict__ X8,
                       uint8_t* __restrict__ S8) {
-  __shared__ float sA[D * D], sB[D], sBp[D];
+  __shared__ __align__(16) float sA[D * D];
+  __shared__ float sB[D], sBp[D];
   __shared__ double red[2][kThreads / 32];
   griddep_wait();  // X, A and B may come from the kernel just before this one
   griddep_launch_dependents();
@@ -46,11 +114,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   if (threadIdx.x < D) sBp[threadIdx.x] = shifted_offset<D>(sA + threadIdx.x * D, sB[threadIdx.x]);
   __syncthreads();
-  float rA[D * D], rBp[D];
-#pragma unroll
-  for (int i = 0; i < D * D; ++i) rA[i] = sA[i];
-#pragma unroll
-  for (int i = 0; i < D; ++i) rBp[i] = sBp[i];
+  if (threadIdx.x < D * D) sA[threadIdx.x] *= 0.03125f;  // see top_block
+  __syncthreads();
 
   const int64_t blocks = d_in / 16, tiles_k = mx::scale_tiles_k(d_in);
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
@@ -91,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if ((lane & 1) == 0) S8[mx::scale_word(m, b >> 3, tiles_k) + ((b >> 1) & 3)] = sb;
 
         uint32_t o[8];
-        float fb, fxr, fxpp;
-        xform_block<D>(u[i][0], u[i][1], rA, rBp, o, fb, fxr, fxpp);
+        float fb, fxr;
+        top_block<D>(u[i][0], u[i][1], sA, sBp, o, fb, fxr);
         st_global_32(Xpp + m * d_in + 16 * b, o);
         s_b += double(fb);
         s_xr += double(fxr);
@@ -111,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         a += red[0][w];
         r += red[1][w];
       }
-      corr[m] = static_cast<float>(a - 1.5 * r);
+      corr[m] = static_cast<float>(a - 5.5 * r);
     }
     __syncthreads();
   }
@@ -121,7 +186,7 @@ template <int D>
 cudaError_t launch_d(const uint16_t* X, int64_t M, int64_t d_in, const float* A, const float* B,
                      uint16_t* Xpp, float* corr, uint8_t* X8, uint8_t* S8, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int64_t most = int64_t(kNumSMsB200) * 2;
+  const int64_t most = int64_t(kNumSMsB200) * 4;  // the CTAs that are resident at once
   cfg.gridDim = dim3(static_cast<unsigned>(M < most ? M : most), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = s;

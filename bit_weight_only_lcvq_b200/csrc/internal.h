@@ -45,8 +45,8 @@ cudaError_t launch_xform_i8(const uint16_t* X, int64_t M, int64_t d_in, int d, c
                             const float* B, uint8_t* X8, float* corr, float* inv_s, cudaStream_t s,
                             int* launches);
 
-// X'' as launch_xform forms it and X packed into mx8, in one pass over X;
-// corr[M] = s' - 3/2 sum_k bf16(X')[m][k]
+// In one pass over X: X packed into mx8, X'' = bf16(X') / 32 in the decoder's order
+// and corr[M] = s' - 11/2 sum_k bf16(X')[m][k]
 cudaError_t launch_xform_ckpt(const uint16_t* X, int64_t M, int64_t d_in, int d, const float* A,
                               const float* B, uint16_t* Xpp, float* corr, uint8_t* X8, uint8_t* S8,
                               cudaStream_t s, int* launches);
@@ -157,9 +157,8 @@ cudaError_t launch_tc_forward(const uint16_t* Xa, bool algebraic, const float* c
                               const uint8_t* packed, int64_t d_out, int64_t d_in, int d,
                               const float* A, const float* B, uint16_t* Y, unsigned int* err,
                               cudaStream_t s, int* launches);
-// the algebraic form without the 128 offset: Y = sum_k X''[m][k] 4^p z[n][k] + corr[m],
-// corr as launch_xform_ckpt writes it
-cudaError_t launch_tc_forward_int(const uint16_t* Xpp, const float* corr, int64_t M,
+// the algebraic form with codes as 128 + 32 z, on X'' and corr of launch_xform_ckpt
+cudaError_t launch_tc_forward_top(const uint16_t* Xpp, const float* corr, int64_t M,
                                   const uint8_t* packed, int64_t d_out, int64_t d_in, uint16_t* Y,
                                   unsigned int* err, cudaStream_t s, int* launches);
 cudaError_t launch_tc_backward_dx(const uint16_t* dY, const float* rsum, int64_t M,

@@ -17,11 +17,15 @@
 // Kinds (D[i][j] = sum_c A[i][c] B[j][c]):
 //   FwdAlg  Y[m][n]  = sum_k X''[m][k] v[n][k] + corr[m]      A = X'' (K-major)
 //           v = 128 + 4^p z: one LOP3 per bf16 pair (see xform.cu)
-//   FwdInt  the same with v = 4^p z: 128 is subtracted from the decoded pairs (one
-//           more instruction each), so that the fp32 sums stay near Y's own size.
-//           With 128 in every term they run 60 times as high, and over a long K the
-//           additions, which the tensor core truncates, show in Y: 2.6e-3 of its
-//           norm against 2.35e-3 at K = 14336 (X' and Y rounded to bf16 make 2.35e-3)
+//   FwdTop  Y[m][n]  = sum_k X''[m][k] v[n][k] + corr[m]      A = X'' (K-major)
+//           v = 128 + 32 z: the code in the top mantissa bits (a shift and a LOP3 per
+//           pair), X'' = bf16(X') / 32.  An offset of 4 beside each z keeps the fp32
+//           sums within 5 times Y's own size; with FwdAlg's up to 128 they run 60
+//           times as high, and over a long K the additions, which the tensor core
+//           truncates, show in Y (8192 x 14336 -> 4096: 2.6e-3 of its norm against
+//           2.35e-3, which X' and Y rounded to bf16 make).  No offset at all (128
+//           subtracted) took 795 us against 720: operands of one exponent switch
+//           less, and the power limit paces this kernel
 //   FwdDec  Y[m][n]  = sum_k X[m][k] bf16(A z + B)[n][k]      A = X (K-major)
 //           decoders evaluate A z + B in fp32 (LC-QAT Methodology 1, c = A z + B)
 //   Dx      P[m][k]  = sum_n dY[m][n] v[n][k]                 A = dY (K-major),
@@ -65,8 +69,8 @@ constexpr int C_BYTES = 4096;         // packed codes of one stage
 constexpr int kPairPeerGroup = 3;
 constexpr int kTmemCols = 512;
 
-enum Kind { kFwdAlg = 0, kFwdDec = 1, kDx = 2, kDw = 3, kGram = 4, kFwdInt = 5 };
-constexpr bool is_alg(int kind) { return kind == kFwdAlg || kind == kFwdInt; }
+enum Kind { kFwdAlg = 0, kFwdDec = 1, kDx = 2, kDw = 3, kGram = 4, kFwdTop = 5 };
+constexpr bool is_alg(int kind) { return kind == kFwdAlg || kind == kFwdTop; }
 
 struct Params {
   int64_t M, N, K;    // D is M x N, contraction K (see each kind)
@@ -124,16 +128,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w)
                : "memory");
-}
-
-// bf16 pairs less 128, exact on the code decoder's 128 + 4^p z
-__device__ __forceinline__ uint4 minus_128(const uint4& v) {
-  auto sub = [](uint32_t a) {
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(0x43004300u));
-    return r;
-  };
-  return make_uint4(sub(v.x), sub(v.y), sub(v.z), sub(v.w));
 }
 
 // One 32-column chunk of a D row (registers r[] from TMEM): the fused
@@ -452,11 +446,8 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint4 c0, c1;
-              dec_word(w[q], c0, c1);
-              if constexpr (KIND == kFwdInt) {
-                c0 = minus_128(c0);
-                c1 = minus_128(c1);
-              }
+              if constexpr (KIND == kFwdTop) dec_word_top(w[q], c0, c1);
+              else dec_word(w[q], c0, c1);
               st_shared_v4(row + (((2 * q) ^ (r & 7)) << 4), c0);
               st_shared_v4(row + (((2 * q + 1) ^ (r & 7)) << 4), c1);
             }
@@ -1109,7 +1100,7 @@ cudaError_t launch_tc_forward(const uint16_t* Xa, bool algebraic, const float* c
   return e;
 }
 
-cudaError_t launch_tc_forward_int(const uint16_t* Xpp, const float* corr, int64_t M,
+cudaError_t launch_tc_forward_top(const uint16_t* Xpp, const float* corr, int64_t M,
                                   const uint8_t* packed, int64_t d_out, int64_t d_in, uint16_t* Y,
                                   unsigned int* err, cudaStream_t s, int* launches) {
   CUtensorMap ta, tb;
@@ -1119,7 +1110,7 @@ cudaError_t launch_tc_forward_int(const uint16_t* Xpp, const float* corr, int64_
   Params p{};
   p.M = M; p.N = d_out; p.K = d_in; p.d_in = d_in; p.d_out = d_out;
   p.codes = packed; p.corr = corr; p.out = Y; p.err = err;
-  cudaError_t e = launch_kind<kFwdInt, 8, kAlgDecWarps>(ta, tb, p, s, nullptr);
+  cudaError_t e = launch_kind<kFwdTop, 8, kAlgDecWarps>(ta, tb, p, s, nullptr);
   ++*launches;
   return e;
 }
