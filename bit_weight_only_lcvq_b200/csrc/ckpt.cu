@@ -2,10 +2,10 @@
 // writes X'' in the decoder's order (see xform.cu), the per-row constant of the
 // integer-code GEMM, and X packed into mx8 (see mx.cuh).
 //
-// The codes enter the GEMM as 128 + 32 z (tc_gemm.cu kind FwdTop), so with
-// X'r = bf16(X') and X'' = X'r / 32
-//     sum_k X''_k (128 + 32 z_k) = sum_k X'r_k z_k + 4 sum_k X'r_k,
-//     Y[m][n] = that + corr,  corr = s' - (3/2 + 4) sum_k X'r_k,
+// The codes enter the GEMM as 128 + 2^b z, b = 3 at even positions and 5 at odd ones
+// (tc_gemm.cu kind FwdTop), so with X'r = bf16(X') and X''_k = X'r_k 2^-b
+//     sum_k X''_k (128 + 2^b z_k) = sum_k X'r_k z_k + 128 sum_k X''_k,
+//     Y[m][n] = that + corr,  corr = s' - 3/2 sum_k X'r_k - 128 sum_k X''_k,
 // s' = sum_g x_g^T (B + 3/2 A 1): the centred algebraic form.
 //
 // Bound by HBM: 2 B an element read, 3.03 written (3.03 read and 5.03 written by
@@ -50,18 +50,20 @@ __device__ __forceinline__ float2 halves(uint64_t v) {
   return r;
 }
 
-// X'' of one 16-element block and its parts of corr, on paired multiply-adds.  sAs
-// is A / 32, a power of two, so rounding commutes with it.
-//   o[c] = bf16x2 of positions c and c + 8;  sb = sum x B';  sxr = 32 sum X''
+// X'' of one 16-element block and its part of corr, on paired multiply-adds.  sAs is A
+// with its even columns / 8 and its odd ones / 32 (d = 1: A): powers of two, so
+// rounding commutes with them.
+//   o[c] = bf16x2 of positions c and c + 8
+//   sb = sum x B';  off = 3/2 sum X'r + 128 sum X''
 template <int D>
 __device__ __forceinline__ void top_block(const uint4& u0, const uint4& u1, const float* sAs,
-                                          const float* sBp, uint32_t (&o)[8], float& sb, float& sxr) {
+                                          const float* sBp, uint32_t (&o)[8], float& sb, float& off) {
   const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
   auto x = [&](int k) { return k & 1 ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1]); };
   float xp[16];
   if constexpr (D == 1) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) xp[k] = x(k) * sAs[0];
+    for (int k = 0; k < 16; ++k) xp[k] = x(k) * (sAs[0] * (k & 1 ? 0.03125f : 0.125f));
   } else {
     constexpr int kV = 16 / D, kJ = D / 2;  // vectors, pairs of columns
     uint64_t acc[kV][kJ] = {};
@@ -89,13 +91,13 @@ __device__ __forceinline__ void top_block(const uint4& u0, const uint4& u1, cons
   sb = 0.f;
 #pragma unroll
   for (int k = 0; k < 16; ++k) sb = fmaf(x(k), sBp[k % D], sb);
-  sxr = 0.f;
+  float part[2] = {0.f, 0.f};  // sums of X'' at even and odd positions
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     o[c] = pack_bf16x2(xp[c], xp[c + 8]);
-    sxr += bf16_lo(o[c]) + bf16_hi(o[c]);
+    part[c & 1] += bf16_lo(o[c]) + bf16_hi(o[c]);
   }
-  sxr *= 32.f;
+  off = (1.5f * 8.f + 128.f) * part[0] + (1.5f * 32.f + 128.f) * part[1];
 }
 
 template <int D>
@@ -114,13 +116,13 @@ __global__ void __launch_bounds__(kThreads, 4)
   __syncthreads();
   if (threadIdx.x < D) sBp[threadIdx.x] = shifted_offset<D>(sA + threadIdx.x * D, sB[threadIdx.x]);
   __syncthreads();
-  if (threadIdx.x < D * D) sA[threadIdx.x] *= 0.03125f;  // see top_block
+  if (D > 1 && threadIdx.x < D * D) sA[threadIdx.x] *= threadIdx.x & 1 ? 0.03125f : 0.125f;  // see top_block
   __syncthreads();
 
   const int64_t blocks = d_in / 16, tiles_k = mx::scale_tiles_k(d_in);
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
     const uint16_t* xr = X + m * d_in;
-    double s_b = 0.0, s_xr = 0.0;
+    double s_b = 0.0, s_off = 0.0;
     for (int64_t b0 = threadIdx.x; b0 - threadIdx.x < blocks; b0 += kAhead * kThreads) {
       uint4 u[kAhead][2];
 #pragma unroll
@@ -156,18 +158,18 @@ __global__ void __launch_bounds__(kThreads, 4)
         if ((lane & 1) == 0) S8[mx::scale_word(m, b >> 3, tiles_k) + ((b >> 1) & 3)] = sb;
 
         uint32_t o[8];
-        float fb, fxr;
-        top_block<D>(u[i][0], u[i][1], sA, sBp, o, fb, fxr);
+        float fb, foff;
+        top_block<D>(u[i][0], u[i][1], sA, sBp, o, fb, foff);
         st_global_32(Xpp + m * d_in + 16 * b, o);
         s_b += double(fb);
-        s_xr += double(fxr);
+        s_off += double(foff);
       }
     }
     s_b = chunk_tree_sum(s_b);
-    s_xr = chunk_tree_sum(s_xr);
+    s_off = chunk_tree_sum(s_off);
     if (lane == 0) {
       red[0][warp] = s_b;
-      red[1][warp] = s_xr;
+      red[1][warp] = s_off;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         a += red[0][w];
         r += red[1][w];
       }
-      corr[m] = static_cast<float>(a - 5.5 * r);
+      corr[m] = static_cast<float>(a - r);
     }
     __syncthreads();
   }

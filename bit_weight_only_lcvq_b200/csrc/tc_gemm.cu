@@ -18,14 +18,14 @@
 //   FwdAlg  Y[m][n]  = sum_k X''[m][k] v[n][k] + corr[m]      A = X'' (K-major)
 //           v = 128 + 4^p z: one LOP3 per bf16 pair (see xform.cu)
 //   FwdTop  Y[m][n]  = sum_k X''[m][k] v[n][k] + corr[m]      A = X'' (K-major)
-//           v = 128 + 32 z: the code in the top mantissa bits (a shift and a LOP3 per
-//           pair), X'' = bf16(X') / 32.  An offset of 4 beside each z keeps the fp32
-//           sums within 5 times Y's own size; with FwdAlg's up to 128 they run 60
-//           times as high, and over a long K the additions, which the tensor core
-//           truncates, show in Y (8192 x 14336 -> 4096: 2.6e-3 of its norm against
-//           2.35e-3, which X' and Y rounded to bf16 make).  No offset at all (128
-//           subtracted) took 795 us against 720: operands of one exponent switch
-//           less, and the power limit paces this kernel
+//           v = 128 + 8 z and 128 + 32 z at even and odd positions (codec.cuh,
+//           dec_word_top; two instructions more per 16 codes), X'' = bf16(X') / 8 and
+//           / 32.  Offsets of 16 and 4 beside z keep the fp32 sums small; with
+//           FwdAlg's 128, 32 and 8 they run 60 times as high as Y, and over a long K
+//           the additions, which the tensor core truncates, show in Y (8192 x 14336
+//           -> 4096: 2.6e-3 of its norm against 2.35e-3, which X' and Y rounded to
+//           bf16 make).  Cleaner decoders cost more, since the power limit paces
+//           this kernel: every code in the top bits 777 us, 128 subtracted 795
 //   FwdDec  Y[m][n]  = sum_k X[m][k] bf16(A z + B)[n][k]      A = X (K-major)
 //           decoders evaluate A z + B in fp32 (LC-QAT Methodology 1, c = A z + B)
 //   Dx      P[m][k]  = sum_n dY[m][n] v[n][k]                 A = dY (K-major),
