@@ -181,6 +181,90 @@ __global__ void __launch_bounds__(kThreads) simt_dx_kernel(
     }
 }
 
+// ---------------------------------------------------------------- few outputs
+// The forward and dX where 64 x 64 tiles would leave most SMs idle: a thread per
+// output in tiles of 16 x 16, the next 64 contraction steps loaded while this one's
+// products run (fp32 activations).  Every output is the same sequence of fused
+// multiply-adds as in the 64 x 64 kernels, so it has the same bits.  16 x 512 x 512:
+// 8.3 us against 25; 32 of the large tiles' work: 24 against 27 (128 x 512 -> 1024)
+// and 45 against 51 (256 x 1024 -> 512), 64 of them: 39 against 27 (512 x 512 -> 512),
+// where their two products per shared-memory read count for more than idle SMs.
+constexpr int kFewT = 16, kFewK = 64;
+constexpr int64_t kFewTiles = 40;
+
+template <int D, bool kForward>  // kForward: C = X W~^T over k; else C = dY W~ over n
+__global__ void __launch_bounds__(kThreads) simt_few_kernel(
+    const float* __restrict__ X, int64_t M, const uint8_t* __restrict__ packed, int64_t N, int64_t K,
+    const float* __restrict__ A, const float* __restrict__ B, float* __restrict__ C) {
+  __shared__ float sA[D * D], sB[D];
+  __shared__ float Xs[2][kFewK][kFewT + 1], Ws[2][kFewK][kFewT + 1];
+  load_AB<D>(A, B, sA, sB);
+  const int tid = threadIdx.x, ty = tid / kFewT, tx = tid % kFewT;
+  const int64_t m0 = int64_t(blockIdx.y) * kFewT, c0 = int64_t(blockIdx.x) * kFewT;
+  const int64_t depth = kForward ? K : N, cols = kForward ? N : K, Kb = K / 4;
+  // this thread's part of a step: four activations, and (half of the threads)
+  // eight weights: forward 16 rows x 64 k, dX 64 rows x 16 k
+  const int xr = tid / 16, xc = tid % 16 * 4;
+  const int wr = kForward ? tid / 8 : tid / 2, wc = kForward ? tid % 8 * 8 : tid % 2 * 8;
+  const bool has_w = tid < 128;
+  float4 xv;
+  uint32_t bits;
+  bool w_in;
+  auto load = [&](int64_t d0) {
+    xv = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m0 + xr < M && d0 + xc < depth)
+      xv = *reinterpret_cast<const float4*>(X + (m0 + xr) * depth + d0 + xc);
+    const int64_t n = kForward ? c0 + wr : d0 + wr, k = kForward ? d0 + wc : c0 + wc;
+    w_in = has_w && n < N;
+    bits = w_in ? codes16(packed, Kb, n, k) : 0u;
+  };
+  auto store = [&](int b) {
+    const float v[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Xs[b][xc + i][xr] = v[i];
+    if (has_w) {
+      float w[8];
+      if (w_in) decode8<D>(bits, sA, sB, w);
+      else for (int i = 0; i < 8; ++i) w[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (kForward) Ws[b][wc + i][wr] = w[i];
+        else Ws[b][wr][wc + i] = w[i];
+      }
+    }
+  };
+  float acc = 0.f;
+  load(0);
+  __syncthreads();  // A, B
+  int b = 0;
+  for (int64_t d0 = 0; d0 < depth; d0 += kFewK, b ^= 1) {
+    store(b);
+    __syncthreads();
+    if (d0 + kFewK < depth) load(d0 + kFewK);
+#pragma unroll
+    for (int kk = 0; kk < kFewK; ++kk) acc = fmaf(Xs[b][kk][ty], Ws[b][kk][tx], acc);
+  }
+  if (m0 + ty < M && c0 + tx < cols) C[(m0 + ty) * cols + c0 + tx] = acc;
+}
+
+bool few_outputs(int64_t M, int64_t cols) { return ceil_div(M, kT) * ceil_div(cols, kT) <= kFewTiles; }
+
+template <bool kForward>
+cudaError_t launch_few(const void* X, int64_t M, const uint8_t* packed, int64_t N, int64_t K, int d,
+                       const float* A, const float* B, void* C, cudaStream_t s) {
+  const int64_t cols = kForward ? N : K;
+  const dim3 grid(static_cast<unsigned>(ceil_div(cols, kFewT)), static_cast<unsigned>(ceil_div(M, kFewT)));
+  const float* x = static_cast<const float*>(X);
+  float* c = static_cast<float*>(C);
+  switch (d) {
+    case 1: simt_few_kernel<1, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
+    case 2: simt_few_kernel<2, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
+    case 4: simt_few_kernel<4, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
+    default: simt_few_kernel<8, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
+  }
+  return cudaGetLastError();
+}
+
 // ---------------------------------------------------------------- dW epilogue
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads) simt_dw_kernel(
@@ -328,6 +412,10 @@ __global__ void __launch_bounds__(256) reduce_partials_kernel(const float* __res
 cudaError_t launch_simt_forward(const void* X, bool bf16, int64_t M, const uint8_t* packed,
                                 int64_t d_out, int64_t d_in, int d, const float* A,
                                 const float* B, void* Y, cudaStream_t s, int* launches) {
+  if (!bf16 && few_outputs(M, d_out)) {
+    ++*launches;
+    return launch_few<true>(X, M, packed, d_out, d_in, d, A, B, Y, s);
+  }
   const dim3 grid(static_cast<unsigned>(ceil_div(d_out, kT)), static_cast<unsigned>(ceil_div(M, kT)));
   LCVQ_DISPATCH_D(d, bf16, simt_forward_kernel, grid, X, M, packed, d_out, d_in, A, B, Y);
   ++*launches;
@@ -337,6 +425,10 @@ cudaError_t launch_simt_forward(const void* X, bool bf16, int64_t M, const uint8
 cudaError_t launch_simt_backward_dx(const void* dY, bool bf16, int64_t M, const uint8_t* packed,
                                     int64_t d_out, int64_t d_in, int d, const float* A,
                                     const float* B, void* dX, cudaStream_t s, int* launches) {
+  if (!bf16 && few_outputs(M, d_in)) {
+    ++*launches;
+    return launch_few<false>(dY, M, packed, d_out, d_in, d, A, B, dX, s);
+  }
   const dim3 grid(static_cast<unsigned>(d_in / kT), static_cast<unsigned>(ceil_div(M, kT)));
   LCVQ_DISPATCH_D(d, bf16, simt_dx_kernel, grid, dY, M, packed, d_out, d_in, A, B, dX);
   ++*launches;

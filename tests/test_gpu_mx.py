@@ -328,6 +328,23 @@ def test_backward_from_kept_x(M, K, N, d, dtype):
     assert torch.equal(part["dA"], g["dA"]) and torch.equal(part["dB"], g["dB"])
 
 
+@pytest.mark.parametrize("d", [1, 2, 4, 8])
+@pytest.mark.parametrize("K,N", [(512, 512), (192, 72), (1088, 136)])
+def test_fp32_rows_do_not_depend_on_their_number(K, N, d):
+    """Few fp32 tokens take smaller tiles; the sums are the same ones in the same
+    order, so every row has the bits it has among thousands."""
+    M = 5000
+    Wp, A, B, x, dy = layer(17, M, K, N, d, F32)
+    packed, mask = lcvq.assign_pack(to_dev(Wp, F32), d)
+    At, Bt, X, dY = to_dev(A, F32), to_dev(B, F32), to_dev(x, F32), to_dev(dy, F32)
+    Y = lcvq.gemm(X, packed, K, At, Bt, d)
+    dX = lcvq.gemm_backward(X, dY, packed, mask, K, At, Bt, d)["dX"]
+    for m in (1, 16, 37):
+        assert torch.equal(lcvq.gemm(X[:m].contiguous(), packed, K, At, Bt, d), Y[:m])
+        g = lcvq.gemm_backward(X[:m].contiguous(), dY[:m].contiguous(), packed, mask, K, At, Bt, d)
+        assert torch.equal(g["dX"], dX[:m])
+
+
 def test_gradient_by_differences():
     """L = sum dY * Y is linear in A and B: (L(A + h E) - L(A - h E)) / 2 h is dA,
     with the kept values as X."""
