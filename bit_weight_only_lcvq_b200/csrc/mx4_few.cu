@@ -134,10 +134,10 @@ __global__ void __launch_bounds__(kThreads)
       ++issued;
       if (++s == C::kStages) { s = 0; ph ^= 1; }
     }
-    if (__shfl_sync(0xffffffffu, *abort_flag, 0) != 0) {  // no copy may land in shared memory after the CTA exits
-      for (int64_t n = issued - 1; n >= 0 && n >= issued - C::kStages; --n)
-        mbar_wait(&full[n % C::kStages], static_cast<uint32_t>((n / C::kStages) & 1), kDefaultWaitLimit);
-    }
+    // no copy may land in shared memory that is used again below or after the CTA
+    // has left (the MMAs have waited for every copy, unless a wait gave up)
+    for (int64_t n = issued - 1; n >= 0 && n >= issued - C::kStages; --n)
+      mbar_wait(&full[n % C::kStages], static_cast<uint32_t>((n / C::kStages) & 1), kDrainLimit);
   } else if (warp == 1) {
     constexpr uint32_t idesc0 = idesc_mxf4(kRows, NT, 0), idesc1 = idesc_mxf4(kRows, NT, 1);
     const uint64_t desc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();                 // the MMAs have completed
   tc_fence_after();
   // every CTA of the cluster is past its copies and MMAs: its stages may be
-  // overwritten (after a wait that gave up, too: the producer has drained them)
+  // overwritten (after a wait that gave up, too: the producer waits for its copies)
   cluster_sync();
   if (warp >= 2) {
     const int quarter = warp & 3;

@@ -79,7 +79,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint64_t* sdrain = drain + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sdrain + 1);
+  // stages whose copies each CTA has issued, and whether the peer gave up a wait
+  volatile int64_t* issued_here = reinterpret_cast<volatile int64_t*>(sdrain + 1);
+  volatile int64_t* peer = issued_here + 1;  // its stages; negative (~stages): it gave up
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sdrain + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -102,6 +105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain, 1);
     mbar_init(sdrain, 1);
+    *issued_here = 0;
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -169,13 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (++s == STAGES) { s = 0; ph ^= 1; }
       }
     }
-    if (warp_abort() && rank == 0) {
-      // no copy may land in shared memory after the CTA exits: the even CTA's
-      // barriers count the bytes of both, and neither CTA leaves before the
-      // cluster barrier at the end
-      for (int64_t n = issued - 1; n >= 0 && n >= issued - STAGES; --n)
-        mbar_wait(&full[n % STAGES], static_cast<uint32_t>((n / STAGES) & 1), kDefaultWaitLimit);
-    }
+    if (lane == 0) *issued_here = issued;
   } else if (warp == 1) {
     if (rank == 0) {
       constexpr uint32_t idesc0 = idesc_mxf4(2 * BM, BN, 0), idesc1 = idesc_mxf4(2 * BM, BN, 1);
@@ -227,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (issued) {  // no MMA may still run when TMEM is released
-        if (elect_one()) mma_commit_pair(drain);
+        if (elect_one()) mma_commit_pair_here(drain);
         __syncwarp();
         if (!mbar_wait(drain, 0, kDefaultWaitLimit)) fail(p, abort_flag, 34);
       }
@@ -260,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tmem_copy_scales_pair(tb + 8 * h, sd + 64 + 32 * h);
               tmem_copy_scales_pair(tb + 8 * h + 4, sd + 128 + 32 * h);
             }
-            mma_commit_pair(&sfull[s]);
+            mma_commit_pair_here(&sfull[s]);
           }
           __syncwarp();
           issued = true;
@@ -274,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (issued) {  // no copy may still run when TMEM is released
-        if (elect_one()) mma_commit_pair(sdrain);
+        if (elect_one()) mma_commit_pair_here(sdrain);
         __syncwarp();
         if (!mbar_wait(sdrain, 0, kDefaultWaitLimit)) fail(p, abort_flag, 37);
       }
@@ -348,7 +346,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) {
+    const int64_t n = *issued_here;
+    st_cluster_u64(mapa_shared(smem_u32(const_cast<int64_t*>(peer)), rank ^ 1),
+                   static_cast<uint64_t>(*abort_flag ? ~n : n));
+  }
+  __syncwarp();
   cluster_sync();  // neither CTA leaves while its peer may still use its shared memory
+  if (*abort_flag || *peer < 0) {
+    // A wait gave up in one of the CTAs: no copy may land in shared memory after
+    // either has left.  The even CTA's barriers count the bytes of both: the bytes
+    // of stages that only one of them issued are made up for, and what was issued
+    // is waited for.
+    if (rank == 0 && threadIdx.x == 0) {
+      const int64_t a = *issued_here, b = *peer < 0 ? ~*peer : *peer;
+      for (int64_t n = b; n < a; ++n) mbar_complete_tx(&full[n % STAGES], STAGE_BYTES);
+      for (int64_t n = a; n < b; ++n) mbar_arrive_expect_tx(&full[n % STAGES], STAGE_BYTES);
+      const int64_t most = a > b ? a : b;
+      for (int64_t n = most - 1; n >= 0 && n >= most - STAGES; --n)
+        mbar_wait(&full[n % STAGES], static_cast<uint32_t>((n / STAGES) & 1), kDrainLimit);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);

@@ -35,6 +35,12 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                "r"(bytes)
                : "memory");
 }
+// counts `bytes` as arrived that no copy will bring
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -68,6 +74,10 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // Limits below this many clock cycles are polled with test_wait: try_wait may
 // suspend the thread in hardware for longer than such a limit.
 constexpr long long kShortWaitLimit = 1LL << 20;
+
+// What a kernel that winds down waits for its own copies in flight, which land in
+// microseconds (about 35 ms).
+constexpr long long kDrainLimit = 1LL << 26;
 
 // Acquire at cluster scope: for barriers that the peer CTA arrives on.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
@@ -176,6 +186,9 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr)
                : "memory");
 }
+__device__ __forceinline__ void st_cluster_u64(uint32_t cluster_addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(cluster_addr), "l"(v) : "memory");
+}
 // 2D tile load by one CTA of a CTA pair; completion is counted on `cluster_bar`,
 // which may be the peer CTA's mbarrier (shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* m, uint32_t cluster_bar,
@@ -265,6 +278,14 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;\n" ::"r"(smem_u32(bar)),
       "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// the same, arriving on this CTA's mbarrier alone
+__device__ __forceinline__ void mma_commit_pair_here(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
+          smem_u32(bar))
       : "memory");
 }
 

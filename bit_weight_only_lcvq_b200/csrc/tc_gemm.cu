@@ -358,11 +358,10 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
         if (++s == STAGES) { s = 0; ph ^= 1; }
       }
     }
-    if (warp_abort()) {  // no copy may land in shared memory after the CTA exits
-      // (the default limit: copies in flight finish in microseconds)
-      for (int64_t n = issued - 1; n >= 0 && n >= issued - STAGES; --n)
-        mbar_wait(&full[n % STAGES], static_cast<uint32_t>((n / STAGES) & 1), kDefaultWaitLimit);
-    }
+    // no copy may land in shared memory after the CTA exits (the consumers have
+    // waited for every copy, unless a wait gave up)
+    for (int64_t n = issued - 1; n >= 0 && n >= issued - STAGES; --n)
+      mbar_wait(&full[n % STAGES], static_cast<uint32_t>((n / STAGES) & 1), kDrainLimit);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, C::kAmn, C::kBmn);
