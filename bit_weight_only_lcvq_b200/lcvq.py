@@ -12,6 +12,7 @@ gemm_backward, workspace_size, check_device_error, mx_pack, mx4_gemm, gemm_ckpt,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -424,16 +425,32 @@ def _mx_rows(t, name: str):
     return (BF16 if dt == torch.bfloat16 else F32), rows, cols, t.device
 
 
-def _on_device(name: str, dev, args, stream):
-    """The C call with dev current (the ABI works on the current device)."""
+def _on_device(name: str, dev, args):
+    """The C call on dev's current stream, with dev current (the ABI works on the
+    current device)."""
     fn, i = getattr(_lib or lib(), name), dev.index
     if i == torch.cuda.current_device():
-        st = fn(*args, _raw_stream(i) if stream is None else stream.cuda_stream)
+        st = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(i) if stream is None else stream.cuda_stream)
+            st = fn(*args, _raw_stream(i))
     if st != 0:
         raise LcvqError(name, st)
+
+
+def _streamed(fn):
+    """fn with a keyword `stream`: made current for the call, so that what the call
+    allocates belongs to it and is not handed out again while its kernels run."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        t = args[0][0] if isinstance(args[0], tuple) else args[0]
+        if t.device != stream.device:
+            raise ValueError(f"lcvq: a stream of {stream.device} for tensors on {t.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _tiles(rows: int, cols: int) -> int:
@@ -445,7 +462,8 @@ def mx_scale_bytes(rows: int, cols: int) -> int:
     return int(lib().lcvq_mx_scale_bytes(rows, cols))
 
 
-def mx_pack(X: torch.Tensor, fmt: str, *, q=None, scales=None, stream=None):
+@_streamed
+def mx_pack(X: torch.Tensor, fmt: str, *, q=None, scales=None):
     """X [rows][cols] (fp32 or bf16, rows contiguous but possibly strided) packed
     into "mx4" or "mx8": (q, scales), see lcvq_mx_pack."""
     dt, rows, cols, dev = _mx_rows(X, "X")
@@ -467,12 +485,13 @@ def mx_pack(X: torch.Tensor, fmt: str, *, q=None, scales=None, stream=None):
     else:
         sp = _need(scales, "scales", _U8, (nb,), dev)
     _on_device("lcvq_mx_pack", dev,
-               (X.data_ptr(), dt, rows, cols, ld if rows > 1 else cols, f, qp, sp), stream)
+               (X.data_ptr(), dt, rows, cols, ld if rows > 1 else cols, f, qp, sp))
     return q, scales
 
 
+@_streamed
 def mx_decode(q: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str, *, dtype=torch.bfloat16,
-              out=None, stream=None) -> torch.Tensor:
+              out=None) -> torch.Tensor:
     """The values [rows][cols] that (q, scales) stand for, exactly."""
     if not q.is_cuda:
         raise ValueError(f"lcvq: expected a CUDA tensor, got one on {q.device}")
@@ -484,12 +503,13 @@ def mx_decode(q: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str, *, dty
         op = out.data_ptr()
     else:
         op = _need(out, "out", out.dtype, (rows, cols), dev)
-    _on_device("lcvq_mx_decode", dev, (qp, sp, rows, cols, f, op, _dtype_code(out.dtype)), stream)
+    _on_device("lcvq_mx_decode", dev, (qp, sp, rows, cols, f, op, _dtype_code(out.dtype)))
     return out
 
 
+@_streamed
 def mx4_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, *,
-             dtype=torch.bfloat16, workspace=None, out=None, stream=None) -> torch.Tensor:
+             dtype=torch.bfloat16, workspace=None, out=None) -> torch.Tensor:
     """Y = X W^T of two "mx4" matrices (see lcvq_mx4_gemm): (xq, xs) the tokens,
     (wq, ws) the weights [d_out][d_in].  Y [M][d_out] in dtype."""
     if not xq.is_cuda:
@@ -504,7 +524,7 @@ def mx4_gemm(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Ten
         op = _need(out, "out", out.dtype, (M, N), dev)
     if workspace is None:
         workspace = new_workspace(workspace_size(OP_MX4_GEMM, out.dtype, M, N, 2 * kb, 8), dev)
-    _on_device("lcvq_mx4_gemm", dev, (*args, op, _dtype_code(out.dtype), *_ws(workspace, dev)), stream)
+    _on_device("lcvq_mx4_gemm", dev, (*args, op, _dtype_code(out.dtype), *_ws(workspace, dev)))
     return out
 
 
@@ -514,8 +534,9 @@ def _layer(packed, d_in, A, B, d, dev):
             _need(A, "A", torch.float32, (d, d), dev), _need(B, "B", torch.float32, (d,), dev))
 
 
+@_streamed
 def gemm_ckpt(X: torch.Tensor, packed: torch.Tensor, d_in: int, A: torch.Tensor, B: torch.Tensor,
-              d: int, *, workspace=None, out=None, kept=None, stream=None):
+              d: int, *, workspace=None, out=None, kept=None):
     """Forward of a training step that keeps X in 8 bits: (Y, kept) with Y = X W~
     and kept = mx_pack(X, "mx8") for gemm_backward_ckpt (see lcvq_gemm_ckpt)."""
     dt, M, _, dev = _mx_rows(X, "X")
@@ -536,13 +557,14 @@ def gemm_ckpt(X: torch.Tensor, packed: torch.Tensor, d_in: int, A: torch.Tensor,
     if workspace is None:
         workspace = new_workspace(workspace_size(OP_GEMM_CKPT, X.dtype, M, d_out, d_in, d), dev)
     _on_device("lcvq_gemm_ckpt", dev,
-               (xp, dt, M, pp, d_out, d_in, d, ap, bp, op, qp, sp, *_ws(workspace, dev)), stream)
+               (xp, dt, M, pp, d_out, d_in, d, ap, bp, op, qp, sp, *_ws(workspace, dev)))
     return out, kept
 
 
+@_streamed
 def gemm_backward_ckpt(kept, dY: torch.Tensor, packed: torch.Tensor, mask, d_in: int,
                        A: torch.Tensor, B: torch.Tensor, d: int, *, want_dx: bool = True,
-                       want_dwp: bool = True, workspace=None, outs=None, stream=None) -> dict:
+                       want_dwp: bool = True, workspace=None, outs=None) -> dict:
     """gemm_backward with X as gemm_ckpt kept it: dict(dX, dA, dB, dWp) (dX / dWp
     None when not wanted; mask may be None then)."""
     dt, M, _, dev = _mx_rows(dY, "dY")
@@ -574,5 +596,5 @@ def gemm_backward_ckpt(kept, dY: torch.Tensor, packed: torch.Tensor, mask, d_in:
     _on_device("lcvq_gemm_backward_ckpt", dev,
                (qp, sp, yp, dt, M, pp, mp, d_out, d_in, d, ap, bp, xp,
                 result("dA", torch.float32, d, d), result("dB", torch.float32, d), wp,
-                *_ws(workspace, dev)), stream)
+                *_ws(workspace, dev)))
     return o

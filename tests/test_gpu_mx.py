@@ -133,7 +133,7 @@ def mx4_operands(seed, M, N, K):
 SHAPES = [(1, 8, 64), (1, 4096, 4096), (2, 520, 192), (7, 136, 1088), (8, 128, 128), (9, 264, 320),
           (16, 1000, 4096), (17, 192, 576), (32, 512, 960), (33, 200, 448), (64, 256, 2048), (77, 520, 1088),
           (128, 192, 256), (129, 384, 704), (200, 1544, 1216), (256, 2048, 512), (513, 776, 1472),
-          (1024, 1600, 64)]
+          (1024, 1600, 64), (200, 8, 64), (129, 16, 128), (128, 8, 320)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -245,6 +245,44 @@ def test_mx4_linear_replays_in_a_graph_and_on_another_stream(M):
     assert torch.equal(y, linear())
     assert not torch.equal(y, first)
     assert lcvq.check_device_error(work) == 0
+
+
+def test_calls_on_a_given_stream():
+    """A `stream` argument takes the whole call there, its allocations too; a stream
+    that is kept busy shows that nothing ran ahead of it."""
+    M, K, N, d = 130, 512, 264, 8
+    Wp, A, B, x, dy = layer(2, M, K, N, d, BF16)
+    packed, mask = lcvq.assign_pack(to_dev(Wp, F32), d)
+    At, Bt, dY = to_dev(A, F32), to_dev(B, F32), to_dev(dy, BF16)
+    X, late = to_dev(np.zeros_like(x), BF16), to_dev(x, BF16)
+    wq, ws = lcvq.mx_pack(to_dev(matrix(3, 72, K, F32), F32), "mx4")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        X.copy_(late)
+    q = lcvq.mx_pack(X, "mx4", stream=side)
+    y4 = lcvq.mx4_gemm(*q, wq, ws, stream=side)
+    Y, kept = lcvq.gemm_ckpt(X, packed, K, At, Bt, d, stream=side)
+    g = lcvq.gemm_backward_ckpt(kept, dY, packed, mask, K, At, Bt, d, stream=side)
+    v = lcvq.mx_decode(*kept, K, "mx8", stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y4, lcvq.mx4_gemm(*lcvq.mx_pack(late, "mx4"), wq, ws))
+    Y1, kept1 = lcvq.gemm_ckpt(late, packed, K, At, Bt, d)
+    g1 = lcvq.gemm_backward_ckpt(kept1, dY, packed, mask, K, At, Bt, d)
+    assert torch.equal(Y, Y1) and all(torch.equal(g[k], g1[k]) for k in g1)
+    assert torch.equal(v, lcvq.mx_decode(*kept1, K, "mx8"))
+
+
+def test_two_products_at_once():
+    """Calls on two streams, each with its own workspace, few and many tokens."""
+    work = [mx4_operands(40 + i, M, 1544, 2048)[:4] for i, M in enumerate((700, 16, 100, 300))]
+    want = [lcvq.mx4_gemm(*w) for w in work]
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    got = [[lcvq.mx4_gemm(*w, stream=s) for w, s in zip(work, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, z) for ys in got for y, z in zip(ys, want))
 
 
 # ---------------------------------------------------------------- X kept in 8 bits
