@@ -130,13 +130,27 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
+// The codes and mask bits of one 32-column chunk of a dW row (zeros outside)
+struct DwBits {
+  uint2 z;
+  uint32_t mask;
+};
+__device__ __forceinline__ DwBits dw_bits(const Params& p, int64_t n, int64_t k0) {
+  DwBits b{make_uint2(0, 0), 0xFFFFFFFFu};
+  if (n < p.M && k0 < p.N) {
+    b.z = *reinterpret_cast<const uint2*>(p.codes + n * (p.d_in / 4) + k0 / 4);
+    if (p.mask != nullptr) b.mask = *reinterpret_cast<const uint32_t*>(p.mask + n * (p.d_in / 8) + k0 / 8);
+  }
+  return b;
+}
+
 // One 32-column chunk of a D row (registers r[] from TMEM): the fused
 // epilogue of each kind.  gm is the D row, gn0 the first D column.
 template <int KIND, int D>
 __device__ __forceinline__ void epilogue_chunk(const Params& p, const float* sAm,
                                                const uint32_t (&r)[32], int64_t gm, int64_t gn0,
                                                float addc, float rs, float (&pa)[D * D],
-                                               float (&pb)[D]) {
+                                               float (&pb)[D], const DwBits& bits) {
   if constexpr (is_alg(KIND) || KIND == kFwdDec) {
     uint16_t* Y = static_cast<uint16_t*>(p.out) + gm * p.N + gn0;
 #pragma unroll
@@ -193,10 +207,8 @@ __device__ __forceinline__ void epilogue_chunk(const Params& p, const float* sAm
     }
   } else {  // kDw: D row = n (d_out), D column = k (d_in)
     const int64_t n = gm, k0 = gn0;
-    const uint2 zc = *reinterpret_cast<const uint2*>(p.codes + n * (p.d_in / 4) + k0 / 4);
-    const uint32_t mb = p.mask != nullptr
-                            ? *reinterpret_cast<const uint32_t*>(p.mask + n * (p.d_in / 8) + k0 / 8)
-                            : 0xFFFFFFFFu;
+    const uint2 zc = bits.z;
+    const uint32_t mb = bits.mask;
     float* dWp = static_cast<float*>(p.out);
     float o[32];
 #pragma unroll
@@ -248,8 +260,8 @@ __device__ __forceinline__ void dw_block_partials(const Params& p, float (&pa)[D
     if (lane == 0) sRed[quarter * NP + e] = x;
   }
   asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the 4 epilogue warps only
-  if (quarter == 0 && lane < 1) {
-    for (int e = 0; e < NP; ++e)
+  if (quarter == 0) {
+    for (int e = lane; e < NP; e += 32)
       p.partials[int64_t(blockIdx.x) * NP + e] =
           ((sRed[e] + sRed[NP + e]) + sRed[2 * NP + e]) + sRed[3 * NP + e];
   }
@@ -542,7 +554,9 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
         tmem_ld_wait();
         const int64_t gn0 = int64_t(nt) * BN + c * 32;  // first D column of the chunk
         if (gm >= p.M || gn0 >= p.N) continue;
-        epilogue_chunk<KIND, D>(p, sAm, r, gm, gn0, addc, rs, pa, pb);
+        DwBits bits{};
+        if constexpr (KIND == kDw) bits = dw_bits(p, gm, gn0);
+        epilogue_chunk<KIND, D>(p, sAm, r, gm, gn0, addc, rs, pa, pb, bits);
       }
       tc_fence_before();
       __syncwarp();
@@ -927,12 +941,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
       tile_coords(tile, m_tiles, n_tiles, kBand, mt, nt);
       const int buf = static_cast<int>(local & 1);
       const uint32_t use = static_cast<uint32_t>(local >> 1);
+      const int64_t gm = int64_t(mt) * 2 * BM + int64_t(rank) * BM + row;
+      // a chunk's codes and mask bits are read one chunk ahead, the first before the
+      // accumulator is there
+      DwBits next{};
+      if constexpr (KIND == kDw) next = dw_bits(p, gm, int64_t(nt) * BN);
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], use & 1, lim))) {  // one outcome per warp
         fail(p, abort_flag, 17);
         break;
       }
       tc_fence_after();
-      const int64_t gm = int64_t(mt) * 2 * BM + int64_t(rank) * BM + row;
       const uint32_t tbase = tmem + buf * BN + (static_cast<uint32_t>(quarter * 32) << 16);
       float addc = 0.f;
       if constexpr (KIND == kFwdAlg) addc = gm < p.M ? p.corr[gm] : 0.f;
@@ -942,10 +960,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
       for (int c = 0; c < BN / 32; ++c) {
         uint32_t r[32];
         tmem_ld32(tbase + c * 32, r);
-        tmem_ld_wait();
         const int64_t gn0 = int64_t(nt) * BN + c * 32;
+        const DwBits bits = next;
+        if constexpr (KIND == kDw)
+          if (c + 1 < BN / 32) next = dw_bits(p, gm, gn0 + 32);
+        tmem_ld_wait();
         if (gm >= p.M || gn0 >= p.N) continue;
-        epilogue_chunk<KIND, D>(p, sAm, r, gm, gn0, addc, rs, pa, pb);
+        epilogue_chunk<KIND, D>(p, sAm, r, gm, gn0, addc, rs, pa, pb, bits);
       }
       tc_fence_before();
       __syncwarp();
