@@ -93,6 +93,9 @@ struct Cfg {
   // codes' arrival to the decoded tile is longer than the MMAs of a k block
   static constexpr int kDecGroups = DW < 8 ? 1 : DW / 4;
   static constexpr int kGroupWarps = DW > 0 ? DW / kDecGroups : 1;
+  // a stage always belongs to one group: a group that came to a stage whose earlier
+  // phases others wait for could take an older phase for the one it needs
+  static_assert(STAGES % kDecGroups == 0, "the groups share the ring's stages out");
   static constexpr bool kHasCodes = KIND != kDw && KIND != kGram;
   static constexpr bool kAmn = KIND == kDw || KIND == kGram;
   static constexpr bool kBmn = KIND == kDx || KIND == kDw || KIND == kGram;
@@ -986,8 +989,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
 
 // ---------------------------------------------------------------- host side
 // decoder warps of the single-CTA kinds (8192 x 14336 -> 4096): dX with one group of
-// four 860 us, with two 790, with three 795; the forward, whose main loop the
-// power limit paces, 770 with one, two or three
+// four 860 us, with two 790; the forward, whose main loop the
+// power limit paces, 770 with one or two
 constexpr int kAlgDecWarps = 4, kDxDecWarps = 8;
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
