@@ -78,14 +78,31 @@ __device__ __forceinline__ void load_AB(const float* A, const float* B, float* s
   for (int i = threadIdx.x; i < D; i += blockDim.x) sB[i] = B[i];
 }
 
+// acc[i][j] += sum over one chunk of P[.][4 ty + i] Q[.][4 tx + j], in chunk order.
+// The chunks are double buffered in shared memory (one barrier each) and the next
+// one's global loads are issued before this one's products (dW and its reduction at
+// 2000 x 1024 -> 1024: 155 us, waiting for each chunk's loads 222).
+__device__ __forceinline__ void mac_step(const float (*P)[kT + 4], const float (*Q)[kT + 4], int ty,
+                                         int tx, float (&acc)[4][4]) {
+#pragma unroll 8
+  for (int kk = 0; kk < kBK; ++kk) {
+    const float4 p = *reinterpret_cast<const float4*>(&P[kk][ty * 4]);
+    const float4 q = *reinterpret_cast<const float4*>(&Q[kk][tx * 4]);
+    const float a[4] = {p.x, p.y, p.z, p.w}, b[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+  }
+}
+
 // ---------------------------------------------------------------- forward
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads) simt_forward_kernel(
     const void* __restrict__ X, int64_t M, const uint8_t* __restrict__ packed, int64_t N,
     int64_t K, const float* __restrict__ A, const float* __restrict__ B, void* __restrict__ Y) {
   __shared__ float sA[D * D], sB[D];
-  __shared__ float Xs[kBK][kT + 4];
-  __shared__ float Ws[kBK][kT + 4];
+  __shared__ __align__(16) float Xs[2][kBK][kT + 4], Ws[2][kBK][kT + 4];
   load_AB<D>(A, B, sA, sB);
   const int tid = threadIdx.x;
   const int64_t m0 = int64_t(blockIdx.y) * kT, n0 = int64_t(blockIdx.x) * kT;
@@ -93,30 +110,26 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(
   const int lrow = tid / 4, lk = (tid % 4) * 8;
   const int64_t Kb = K / 4;
   float acc[4][4] = {};
-  __syncthreads();
-  for (int64_t k0 = 0; k0 < K; k0 += kBK) {
-    float xv[8], wv[8];
+  float xv[8] = {};
+  uint32_t bits = 0;
+  auto load = [&](int64_t k0) {  // this thread's part of the next step
     if (m0 + lrow < M) load8<kBf16>(X, (m0 + lrow) * K + k0 + lk, xv);
-    else for (int i = 0; i < 8; ++i) xv[i] = 0.f;
-    if (n0 + lrow < N) decode8<D>(codes16(packed, Kb, n0 + lrow, k0 + lk), sA, sB, wv);
-    else for (int i = 0; i < 8; ++i) wv[i] = 0.f;
+    if (n0 + lrow < N) bits = codes16(packed, Kb, n0 + lrow, k0 + lk);
+  };
+  load(0);
+  __syncthreads();
+  int b = 0;
+  for (int64_t k0 = 0; k0 < K; k0 += kBK, b ^= 1) {
+    float wv[8] = {};
+    if (n0 + lrow < N) decode8<D>(bits, sA, sB, wv);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      Xs[lk + i][lrow] = xv[i];
-      Ws[lk + i][lrow] = wv[i];
+      Xs[b][lk + i][lrow] = xv[i];
+      Ws[b][lk + i][lrow] = wv[i];
     }
     __syncthreads();
-#pragma unroll 8
-    for (int kk = 0; kk < kBK; ++kk) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { a[i] = Xs[kk][ty * 4 + i]; b[i] = Ws[kk][tx * 4 + i]; }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
+    if (k0 + kBK < K) load(k0 + kBK);
+    mac_step(Xs[b], Ws[b], ty, tx, acc);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -133,44 +146,40 @@ __global__ void __launch_bounds__(kThreads) simt_dx_kernel(
     const void* __restrict__ dY, int64_t M, const uint8_t* __restrict__ packed, int64_t N,
     int64_t K, const float* __restrict__ A, const float* __restrict__ B, void* __restrict__ dX) {
   __shared__ float sA[D * D], sB[D];
-  __shared__ float Ds[kBK][kT + 4];  // [n][m]
-  __shared__ float Ws[kBK][kT + 4];  // [n][k]
+  __shared__ __align__(16) float Ds[2][kBK][kT + 4];  // [n][m]
+  __shared__ __align__(16) float Ws[2][kBK][kT + 4];  // [n][k]
   load_AB<D>(A, B, sA, sB);
   const int tid = threadIdx.x;
   const int64_t m0 = int64_t(blockIdx.y) * kT, k0 = int64_t(blockIdx.x) * kT;
   const int ty = tid / 16, tx = tid % 16;
   const int64_t Kb = K / 4;
   float acc[4][4] = {};
+  const int lm = tid / 4, lnd = (tid % 4) * 8;  // dY tile: 64 m x 32 n
+  const int lnw = tid / 8, lk = (tid % 8) * 8;  // W~ tile: 32 n x 64 k
+  float v[8];
+  uint32_t bits;
+  bool w_in;
+  auto load = [&](int64_t nb) {  // this thread's part of the next step
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    if (m0 + lm < M && nb + lnd < N) load8<kBf16>(dY, (m0 + lm) * N + nb + lnd, v);
+    w_in = nb + lnw < N;
+    bits = w_in ? codes16(packed, Kb, nb + lnw, k0 + lk) : 0u;
+  };
+  load(0);
   __syncthreads();
-  for (int64_t nb = 0; nb < N; nb += kBK) {
-    {  // dY tile: 64 m x 32 n
-      const int lm = tid / 4, ln = (tid % 4) * 8;
-      float v[8];
-      if (m0 + lm < M && nb + ln < N) load8<kBf16>(dY, (m0 + lm) * N + nb + ln, v);
-      else for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  int b = 0;
+  for (int64_t nb = 0; nb < N; nb += kBK, b ^= 1) {
+    float w[8] = {};
+    if (w_in) decode8<D>(bits, sA, sB, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) Ds[ln + i][lm] = v[i];
-    }
-    {  // W~ tile: 32 n x 64 k
-      const int ln = tid / 8, lk = (tid % 8) * 8;
-      float w[8];
-      if (nb + ln < N) decode8<D>(codes16(packed, Kb, nb + ln, k0 + lk), sA, sB, w);
-      else for (int i = 0; i < 8; ++i) w[i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) Ws[ln][lk + i] = w[i];
+    for (int i = 0; i < 8; ++i) {
+      Ds[b][lnd + i][lm] = v[i];
+      Ws[b][lnw][lk + i] = w[i];
     }
     __syncthreads();
-#pragma unroll 8
-    for (int nn = 0; nn < kBK; ++nn) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { a[i] = Ds[nn][ty * 4 + i]; b[i] = Ws[nn][tx * 4 + i]; }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
+    if (nb + kBK < N) load(nb + kBK);
+    mac_step(Ds[b], Ws[b], ty, tx, acc);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -181,88 +190,125 @@ __global__ void __launch_bounds__(kThreads) simt_dx_kernel(
     }
 }
 
-// ---------------------------------------------------------------- few outputs
-// The forward and dX where 64 x 64 tiles would leave most SMs idle: a thread per
-// output in tiles of 16 x 16, the next 64 contraction steps loaded while this one's
-// products run (fp32 activations).  Every output is the same sequence of fused
-// multiply-adds as in the 64 x 64 kernels, so it has the same bits.  16 x 512 x 512:
-// 8.3 us against 25; 32 of the large tiles' work: 24 against 27 (128 x 512 -> 1024)
-// and 45 against 51 (256 x 1024 -> 512), 64 of them: 39 against 27 (512 x 512 -> 512),
-// where their two products per shared-memory read count for more than idle SMs.
-constexpr int kFewT = 16, kFewK = 64;
-constexpr int64_t kFewTiles = 40;
+// ---------------------------------------------------------------- smaller tiles
+// The forward and dX (fp32 activations) in tiles of kTile x kTile outputs, kTile / 16
+// squared per thread, the next 64 contraction steps loaded while this one's products
+// run.  Every output is the same sequence of fused multiply-adds as in the 64 x 64
+// kernels, so it has the same bits whatever the tile.  16: a row's 64 steps are read
+// by 16 lanes.  32: a thread reads whole sectors of one row and a warp's lanes take
+// different rows, so that the transposed stores hit different banks (in the 64 x 64
+// kernels they meet four at a time).
+constexpr int kDeep = 64;  // contraction steps per chunk
 
-template <int D, bool kForward>  // kForward: C = X W~^T over k; else C = dY W~ over n
-__global__ void __launch_bounds__(kThreads) simt_few_kernel(
+template <int D, int kTile, bool kForward>  // kForward: C = X W~^T over k; else C = dY W~ over n
+__global__ void __launch_bounds__(kThreads) simt_tile_kernel(
     const float* __restrict__ X, int64_t M, const uint8_t* __restrict__ packed, int64_t N, int64_t K,
     const float* __restrict__ A, const float* __restrict__ B, float* __restrict__ C) {
+  constexpr int kR = kTile / 16;     // outputs per thread and dimension
+  constexpr int kPitch = kTile == 16 ? 17 : 36;
+  constexpr int kX = kTile * kDeep / kThreads;  // activations staged per thread: 4 or 8
+  static_assert(kTile == 16 || kTile == 32, "tiles");
   __shared__ float sA[D * D], sB[D];
-  __shared__ float Xs[2][kFewK][kFewT + 1], Ws[2][kFewK][kFewT + 1];
+  __shared__ __align__(16) float Xs[2][kDeep][kPitch], Ws[2][kDeep][kPitch];
   load_AB<D>(A, B, sA, sB);
-  const int tid = threadIdx.x, ty = tid / kFewT, tx = tid % kFewT;
-  const int64_t m0 = int64_t(blockIdx.y) * kFewT, c0 = int64_t(blockIdx.x) * kFewT;
+  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const int64_t m0 = int64_t(blockIdx.y) * kTile, c0 = int64_t(blockIdx.x) * kTile;
   const int64_t depth = kForward ? K : N, cols = kForward ? N : K, Kb = K / 4;
-  // this thread's part of a step: four activations, and (half of the threads)
-  // eight weights: forward 16 rows x 64 k, dX 64 rows x 16 k
-  const int xr = tid / 16, xc = tid % 16 * 4;
-  const int wr = kForward ? tid / 8 : tid / 2, wc = kForward ? tid % 8 * 8 : tid % 2 * 8;
-  const bool has_w = tid < 128;
-  float4 xv;
-  uint32_t bits;
-  bool w_in;
+  const int xr = kTile == 16 ? tid / 16 : tid % kTile;
+  const int xc = kTile == 16 ? tid % 16 * 4 : tid / kTile * kX;
+  // eight weights: forward kTile rows x 64 k, dX 64 rows x kTile k
+  const int wr = !kForward ? tid / (kTile / 8) : (kTile == 16 ? tid / 8 : tid % kTile);
+  const int wc = !kForward ? tid % (kTile / 8) * 8 : (kTile == 16 ? tid % 8 * 8 : tid / kTile * 8);
+  const bool has_w = tid < kTile * 8;
+  float xv[kX];
+  uint32_t bits = 0;
+  bool w_in = false;
   auto load = [&](int64_t d0) {
-    xv = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m0 + xr < M && d0 + xc < depth)
-      xv = *reinterpret_cast<const float4*>(X + (m0 + xr) * depth + d0 + xc);
+#pragma unroll
+    for (int q = 0; q < kX; q += 4) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (m0 + xr < M && d0 + xc + q < depth)
+        v = *reinterpret_cast<const float4*>(X + (m0 + xr) * depth + d0 + xc + q);
+      xv[q] = v.x; xv[q + 1] = v.y; xv[q + 2] = v.z; xv[q + 3] = v.w;
+    }
     const int64_t n = kForward ? c0 + wr : d0 + wr, k = kForward ? d0 + wc : c0 + wc;
-    w_in = has_w && n < N;
+    w_in = has_w && n < N && k < K;
     bits = w_in ? codes16(packed, Kb, n, k) : 0u;
   };
   auto store = [&](int b) {
-    const float v[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) Xs[b][xc + i][xr] = v[i];
+    for (int i = 0; i < kX; ++i) Xs[b][xc + i][xr] = xv[i];
     if (has_w) {
-      float w[8];
+      float w[8] = {};
       if (w_in) decode8<D>(bits, sA, sB, w);
-      else for (int i = 0; i < 8; ++i) w[i] = 0.f;
+      if constexpr (kForward) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (kForward) Ws[b][wc + i][wr] = w[i];
-        else Ws[b][wr][wc + i] = w[i];
+        for (int i = 0; i < 8; ++i) Ws[b][wc + i][wr] = w[i];
+      } else if constexpr (kTile == 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) Ws[b][wr][wc + i] = w[i];
+      } else {
+        float4* o = reinterpret_cast<float4*>(&Ws[b][wr][wc]);
+        o[0] = make_float4(w[0], w[1], w[2], w[3]);
+        o[1] = make_float4(w[4], w[5], w[6], w[7]);
       }
     }
   };
-  float acc = 0.f;
+  float acc[kR][kR] = {};
   load(0);
   __syncthreads();  // A, B
   int b = 0;
-  for (int64_t d0 = 0; d0 < depth; d0 += kFewK, b ^= 1) {
+  for (int64_t d0 = 0; d0 < depth; d0 += kDeep, b ^= 1) {
     store(b);
     __syncthreads();
-    if (d0 + kFewK < depth) load(d0 + kFewK);
+    if (d0 + kDeep < depth) load(d0 + kDeep);
 #pragma unroll
-    for (int kk = 0; kk < kFewK; ++kk) acc = fmaf(Xs[b][kk][ty], Ws[b][kk][tx], acc);
+    for (int kk = 0; kk < kDeep; ++kk) {
+      float a[kR], w[kR];
+      if constexpr (kR == 2) {
+        const float2 p = *reinterpret_cast<const float2*>(&Xs[b][kk][2 * ty]);
+        const float2 q = *reinterpret_cast<const float2*>(&Ws[b][kk][2 * tx]);
+        a[0] = p.x; a[1] = p.y; w[0] = q.x; w[1] = q.y;
+      } else {
+        a[0] = Xs[b][kk][ty];
+        w[0] = Ws[b][kk][tx];
+      }
+#pragma unroll
+      for (int i = 0; i < kR; ++i)
+#pragma unroll
+        for (int j = 0; j < kR; ++j) acc[i][j] = fmaf(a[i], w[j], acc[i][j]);
+    }
   }
-  if (m0 + ty < M && c0 + tx < cols) C[(m0 + ty) * cols + c0 + tx] = acc;
+#pragma unroll
+  for (int i = 0; i < kR; ++i)
+#pragma unroll
+    for (int j = 0; j < kR; ++j) {
+      const int64_t m = m0 + ty * kR + i, c = c0 + tx * kR + j;
+      if (m < M && c < cols) C[m * cols + c] = acc[i][j];
+    }
 }
 
-bool few_outputs(int64_t M, int64_t cols) { return ceil_div(M, kT) * ceil_div(cols, kT) <= kFewTiles; }
-
-template <bool kForward>
-cudaError_t launch_few(const void* X, int64_t M, const uint8_t* packed, int64_t N, int64_t K, int d,
-                       const float* A, const float* B, void* C, cudaStream_t s) {
-  const int64_t cols = kForward ? N : K;
-  const dim3 grid(static_cast<unsigned>(ceil_div(cols, kFewT)), static_cast<unsigned>(ceil_div(M, kFewT)));
-  const float* x = static_cast<const float*>(X);
-  float* c = static_cast<float*>(C);
+template <int kTile, bool kForward>
+cudaError_t launch_tile(const float* x, int64_t M, const uint8_t* packed, int64_t N, int64_t K, int d,
+                        const float* A, const float* B, float* c, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(kForward ? N : K, kTile)),
+                  static_cast<unsigned>(ceil_div(M, kTile)));
   switch (d) {
-    case 1: simt_few_kernel<1, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
-    case 2: simt_few_kernel<2, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
-    case 4: simt_few_kernel<4, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
-    default: simt_few_kernel<8, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
+    case 1: simt_tile_kernel<1, kTile, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
+    case 2: simt_tile_kernel<2, kTile, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
+    case 4: simt_tile_kernel<4, kTile, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
+    default: simt_tile_kernel<8, kTile, kForward><<<grid, kThreads, 0, s>>>(x, M, packed, N, K, A, B, c); break;
   }
   return cudaGetLastError();
+}
+
+// The tile: the largest that still gives the SMs one or two CTAs each.  Measured
+// (16, 32, 64): 16 x 512 -> 512 7.8, 12.9, 24 us; 128 x 512 -> 1024 23, 14.5, 25;
+// 100 x 1024 -> 1024 44, 28, 47; 512 x 512 -> 512 39, 25, 25; 512 x 1024 -> 1024 148, 92, 47.
+int tile_of(int64_t M, int64_t cols) {
+  if (ceil_div(M, 16) * ceil_div(cols, 16) <= kNumSMsB200) return 16;
+  if (ceil_div(M, 32) * ceil_div(cols, 32) <= 2 * kNumSMsB200) return 32;
+  return 64;
 }
 
 // ---------------------------------------------------------------- dW epilogue
@@ -273,43 +319,37 @@ __global__ void __launch_bounds__(kThreads) simt_dw_kernel(
     const float* __restrict__ A, float* __restrict__ dWp, float* __restrict__ partials) {
   constexpr int NP = D * D + D;
   __shared__ float sA[D * D];
-  __shared__ float buf[2][kBK][kT + 4];  // [0]: dY tile [m][n]; [1]: X tile [m][k]; then G
+  __shared__ __align__(16) float buf[2][2][kBK][kT + 4];  // dY tiles [m][n], X tiles [m][k]; then G
   __shared__ float red[kThreads / 32][NP];
-  float (*Ds)[kT + 4] = buf[0];
-  float (*Xs)[kT + 4] = buf[1];
   for (int i = threadIdx.x; i < D * D; i += blockDim.x) sA[i] = A[i];
   const int tid = threadIdx.x;
   const int64_t n0 = int64_t(blockIdx.y) * kT, k0 = int64_t(blockIdx.x) * kT;
   const int ty = tid / 16, tx = tid % 16;
   const int64_t Kb = K / 4;
   float acc[4][4] = {};
-  __syncthreads();
-  for (int64_t mb = 0; mb < M; mb += kBK) {
-    const int lm = tid / 8, lc = (tid % 8) * 8;
-    float v[8];
-    if (mb + lm < M && n0 + lc < N) load8<kBf16>(dY, (mb + lm) * N + n0 + lc, v);
-    else for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  const int lm = tid / 8, lc = (tid % 8) * 8;
+  float dv[8], xv[8];
+  auto load = [&](int64_t mb) {  // this thread's part of the next step
 #pragma unroll
-    for (int i = 0; i < 8; ++i) Ds[lm][lc + i] = v[i];
-    if (mb + lm < M) load8<kBf16>(X, (mb + lm) * K + k0 + lc, v);
-    else for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    for (int i = 0; i < 8; ++i) dv[i] = xv[i] = 0.f;
+    if (mb + lm < M && n0 + lc < N) load8<kBf16>(dY, (mb + lm) * N + n0 + lc, dv);
+    if (mb + lm < M) load8<kBf16>(X, (mb + lm) * K + k0 + lc, xv);
+  };
+  load(0);
+  int b = 0;
+  for (int64_t mb = 0; mb < M; mb += kBK, b ^= 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) Xs[lm][lc + i] = v[i];
-    __syncthreads();
-#pragma unroll 8
-    for (int mm = 0; mm < kBK; ++mm) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { a[i] = Ds[mm][ty * 4 + i]; b[i] = Xs[mm][tx * 4 + i]; }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    for (int i = 0; i < 8; ++i) {
+      buf[0][b][lm][lc + i] = dv[i];
+      buf[1][b][lm][lc + i] = xv[i];
     }
     __syncthreads();
+    if (mb + kBK < M) load(mb + kBK);
+    mac_step(buf[0][b], buf[1][b], ty, tx, acc);
   }
-  // G tile -> shared memory, reusing the operand buffers (64 x 65 <= 2 x 32 x 68 floats)
-  float* Gs = &buf[0][0][0];
+  __syncthreads();
+  // G tile -> shared memory, reusing the operand buffers (64 x 65 <= 4 x 32 x 68 floats)
+  float* Gs = &buf[0][0][0][0];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -412,9 +452,12 @@ __global__ void __launch_bounds__(256) reduce_partials_kernel(const float* __res
 cudaError_t launch_simt_forward(const void* X, bool bf16, int64_t M, const uint8_t* packed,
                                 int64_t d_out, int64_t d_in, int d, const float* A,
                                 const float* B, void* Y, cudaStream_t s, int* launches) {
-  if (!bf16 && few_outputs(M, d_out)) {
+  if (const int tile = bf16 ? 64 : tile_of(M, d_out); tile < 64) {
     ++*launches;
-    return launch_few<true>(X, M, packed, d_out, d_in, d, A, B, Y, s);
+    const float* x = static_cast<const float*>(X);
+    float* y = static_cast<float*>(Y);
+    return tile == 16 ? launch_tile<16, true>(x, M, packed, d_out, d_in, d, A, B, y, s)
+                      : launch_tile<32, true>(x, M, packed, d_out, d_in, d, A, B, y, s);
   }
   const dim3 grid(static_cast<unsigned>(ceil_div(d_out, kT)), static_cast<unsigned>(ceil_div(M, kT)));
   LCVQ_DISPATCH_D(d, bf16, simt_forward_kernel, grid, X, M, packed, d_out, d_in, A, B, Y);
@@ -425,9 +468,12 @@ cudaError_t launch_simt_forward(const void* X, bool bf16, int64_t M, const uint8
 cudaError_t launch_simt_backward_dx(const void* dY, bool bf16, int64_t M, const uint8_t* packed,
                                     int64_t d_out, int64_t d_in, int d, const float* A,
                                     const float* B, void* dX, cudaStream_t s, int* launches) {
-  if (!bf16 && few_outputs(M, d_in)) {
+  if (const int tile = bf16 ? 64 : tile_of(M, d_in); tile < 64) {
     ++*launches;
-    return launch_few<false>(dY, M, packed, d_out, d_in, d, A, B, dX, s);
+    const float* y = static_cast<const float*>(dY);
+    float* x = static_cast<float*>(dX);
+    return tile == 16 ? launch_tile<16, false>(y, M, packed, d_out, d_in, d, A, B, x, s)
+                      : launch_tile<32, false>(y, M, packed, d_out, d_in, d, A, B, x, s);
   }
   const dim3 grid(static_cast<unsigned>(d_in / kT), static_cast<unsigned>(ceil_div(M, kT)));
   LCVQ_DISPATCH_D(d, bf16, simt_dx_kernel, grid, dY, M, packed, d_out, d_in, A, B, dX);

@@ -378,7 +378,7 @@ def test_fp32_rows_do_not_depend_on_their_number(K, N, d):
     At, Bt, X, dY = to_dev(A, F32), to_dev(B, F32), to_dev(x, F32), to_dev(dy, F32)
     Y = lcvq.gemm(X, packed, K, At, Bt, d)
     dX = lcvq.gemm_backward(X, dY, packed, mask, K, At, Bt, d)["dX"]
-    for m in (1, 16, 37):
+    for m in (1, 16, 37, 190, 330):
         assert torch.equal(lcvq.gemm(X[:m].contiguous(), packed, K, At, Bt, d), Y[:m])
         g = lcvq.gemm_backward(X[:m].contiguous(), dY[:m].contiguous(), packed, mask, K, At, Bt, d)
         assert torch.equal(g["dX"], dX[:m])
