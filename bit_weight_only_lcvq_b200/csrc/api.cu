@@ -457,12 +457,14 @@ lcvq_status lcvq_gemm_xformed(const void* Xpp, const float* corr, int64_t M,
   return finish(e, launches);
 }
 
-lcvq_status lcvq_gemm_backward(const void* X, const void* dY, lcvq_dtype dtype, int64_t M,
-                               const uint8_t* packed, const uint8_t* mask_bits, int64_t d_out,
-                               int64_t d_in, int d, const float* A, const float* B, void* dX,
-                               float* dA, float* dB, float* dWp, void* workspace,
-                               size_t ws_bytes, void* stream) {
-  LCVQ_API_RANGE();
+// The backward; with X8 set, X is scratch for the values that X8 and S8 stand for
+// (written between the row sums and the first GEMM, so that every kernel after them
+// overlaps its setup with the one before).
+static lcvq_status run_backward(const void* X, const uint8_t* X8, const uint8_t* S8, const void* dY,
+                                lcvq_dtype dtype, int64_t M, const uint8_t* packed,
+                                const uint8_t* mask_bits, int64_t d_out, int64_t d_in, int d,
+                                const float* A, const float* B, void* dX, float* dA, float* dB,
+                                float* dWp, void* workspace, size_t ws_bytes, void* stream) {
   if (lcvq_status st = validate_gemm_shapes(dtype, M, d_out, d_in, d); st != LCVQ_OK) return st;
   g_last_launches = 0;
   if (!dA || !dB) return LCVQ_ERR_INVALID_ARG;
@@ -500,8 +502,10 @@ lcvq_status lcvq_gemm_backward(const void* X, const void* dY, lcvq_dtype dtype, 
   if (dtype == LCVQ_BF16) {
     float* rsum = reinterpret_cast<float*>(ws + w.rsum_off);
     const uint16_t* dYb = static_cast<const uint16_t*>(dY);
+    if (dX) e = launch_rowsum(dYb, M, d_out, rsum, s, &launches);
+    if (e == cudaSuccess && X8)
+      e = launch_mx_decode(X8, S8, M, d_in, false, const_cast<void*>(X), false, s, &launches);
     if (dX) {
-      e = launch_rowsum(dYb, M, d_out, rsum, s, &launches);
       if (e == cudaSuccess)
         e = launch_tc_backward_dx(dYb, rsum, M, packed, d_out, d_in, d, A, B,
                                   static_cast<uint16_t*>(dX), err, s, &launches);
@@ -512,7 +516,9 @@ lcvq_status lcvq_gemm_backward(const void* X, const void* dY, lcvq_dtype dtype, 
                                 d_in, d, A, dWp, partials, &grid, err, s, &launches);
     parts = grid;
   } else {
-    if (dX) e = launch_simt_backward_dx(dY, false, M, packed, d_out, d_in, d, A, B, dX, s, &launches);
+    if (X8) e = launch_mx_decode(X8, S8, M, d_in, false, const_cast<void*>(X), true, s, &launches);
+    if (e == cudaSuccess && dX)
+      e = launch_simt_backward_dx(dY, false, M, packed, d_out, d_in, d, A, B, dX, s, &launches);
     if (e == cudaSuccess)
       e = launch_simt_backward_dw(X, dY, false, M, packed, mask_bits, d_out, d_in, d, A, dWp,
                                   partials, s, &launches);
@@ -520,6 +526,16 @@ lcvq_status lcvq_gemm_backward(const void* X, const void* dY, lcvq_dtype dtype, 
   }
   if (e == cudaSuccess) e = launch_reduce_partials(partials, parts, d, dA, dB, s, &launches);
   return finish(e, launches);
+}
+
+lcvq_status lcvq_gemm_backward(const void* X, const void* dY, lcvq_dtype dtype, int64_t M,
+                               const uint8_t* packed, const uint8_t* mask_bits, int64_t d_out,
+                               int64_t d_in, int d, const float* A, const float* B, void* dX,
+                               float* dA, float* dB, float* dWp, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  LCVQ_API_RANGE();
+  return run_backward(X, nullptr, nullptr, dY, dtype, M, packed, mask_bits, d_out, d_in, d, A, B, dX,
+                      dA, dB, dWp, workspace, ws_bytes, stream);
 }
 
 size_t lcvq_mx_scale_bytes(int64_t rows, int64_t cols) {
@@ -654,8 +670,8 @@ lcvq_status lcvq_gemm_backward_ckpt(const uint8_t* X8, const uint8_t* S8, const 
   g_last_launches = 0;
   if (lcvq_status st = validate_gemm_shapes(dtype, M, d_out, d_in, d); st != LCVQ_OK) return st;
   if (M == 0 || d_out == 0 || d_in == 0)  // empty sums: X is not read
-    return lcvq_gemm_backward(nullptr, dY, dtype, M, packed, mask_bits, d_out, d_in, d, A, B, dX, dA,
-                              dB, dWp, workspace, ws_bytes, stream);
+    return run_backward(nullptr, nullptr, nullptr, dY, dtype, M, packed, mask_bits, d_out, d_in, d, A,
+                        B, dX, dA, dB, dWp, workspace, ws_bytes, stream);
   if (lcvq_status st = validate_mx(M, d_in, LCVQ_MX8, dtype); st != LCVQ_OK) return st;
   if (!dA || !dB || (dWp && !mask_bits)) return LCVQ_ERR_INVALID_ARG;
   if (!X8 || !S8 || !dY || !packed || !A || !B || !workspace) return LCVQ_ERR_INVALID_ARG;
@@ -666,16 +682,8 @@ lcvq_status lcvq_gemm_backward_ckpt(const uint8_t* X8, const uint8_t* S8, const 
   if (ws_bytes < bwd_ckpt_ws(dtype, M, d_out, d_in, d)) return LCVQ_ERR_WORKSPACE;
   if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
   const size_t off = bwd_ckpt_values_off(M, d_out, d_in, d);
-  void* X = static_cast<char*>(workspace) + off;
-  int launches = 0;
-  cudaError_t e = launch_mx_decode(X8, S8, M, d_in, false, X, dtype == LCVQ_F32,
-                                   static_cast<cudaStream_t>(stream), &launches);
-  if (e != cudaSuccess) return LCVQ_ERR_CUDA;
-  lcvq_status st = lcvq_gemm_backward(X, dY, dtype, M, packed, mask_bits, d_out, d_in, d, A, B, dX,
-                                      dA, dB, dWp, workspace, off, stream);
-  if (st != LCVQ_OK) return st;
-  g_last_launches += launches;
-  return LCVQ_OK;
+  return run_backward(static_cast<char*>(workspace) + off, X8, S8, dY, dtype, M, packed, mask_bits,
+                      d_out, d_in, d, A, B, dX, dA, dB, dWp, workspace, off, stream);
 }
 
 lcvq_status lcvq_check_device_error(void* workspace, void* stream) {

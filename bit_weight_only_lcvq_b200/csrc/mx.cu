@@ -17,6 +17,7 @@
 #include "internal.h"
 #include "mx.cuh"
 #include "mx_pack.cuh"
+#include "pdl.cuh"
 
 namespace lcvq {
 
@@ -136,22 +137,6 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), int64_t grid, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...); e != cudaSuccess)
-    return e;
-  return cudaGetLastError();
-}
-
 // Pieces of a row that a warp takes: four from one CTA per SM on (bf16 2048 x 4096 to
 // mx4 5.3 us against 7.0 with one, 512 x 4096 2.3 against 2.7; 256 x 4096, below that,
 // 1.9 with either), unless the last four would mostly lie beyond the row (mx8
@@ -171,7 +156,7 @@ cudaError_t launch_mx_pack(const void* X, bool f32, int64_t rows, int64_t cols, 
   const int64_t segs = segments(cols, many ? kUnits : 1), grid = ceil_div(rows * segs, kWarps);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, s, X, ld, rows, cols, static_cast<int>(segs), q, scales);
+    return launch_pdl(kern, grid, kThreads, 0, s, X, ld, rows, cols, static_cast<int>(segs), q, scales);
   };
   ++*launches;
   if (mx4) {
@@ -188,7 +173,7 @@ cudaError_t launch_mx_decode(const uint8_t* q, const uint8_t* scales, int64_t ro
   const int64_t segs = segments(cols, many ? kUnits : 1), grid = ceil_div(rows * segs, kWarps);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kern) {
-    return launch_pdl(kern, grid, s, q, scales, rows, cols, static_cast<int>(segs), out);
+    return launch_pdl(kern, grid, kThreads, 0, s, q, scales, rows, cols, static_cast<int>(segs), out);
   };
   ++*launches;
   if (mx4) {

@@ -11,6 +11,9 @@
 // rows to the CTA of the cluster that owns those rows (distributed shared
 // memory), and after one cluster barrier the owner adds them in CTA order and
 // writes Y: one launch, no scratch in memory, the same bits every time.
+// Measured (graph replay): 1 x 4096 -> 4096 5.3 us, 16 x 4096 -> 11008 6.5 us,
+// 1 x 14336 -> 14336 19.1 us (5.7 TB/s of packed weights).  Decoding to bytes for the
+// integer MMA of a warp instead took 9.8, 20.5 and 63 us, bound by its instructions.
 //
 //   warp 0      producer (TMA boxes of W, X and their scale tiles)
 //   warp 1      TMEM allocation, scale copies, MMA issue

@@ -14,7 +14,9 @@
 // W~ tiles are decoded on chip from the packed codes (A z + B in fp32, a fixed
 // FMA order) and never written to memory.
 #include "common.cuh"
+#include "gemv_common.cuh"
 #include "internal.h"
+#include "pdl.cuh"
 
 namespace lcvq {
 
@@ -413,14 +415,16 @@ __global__ void __launch_bounds__(kThreads) simt_dw_kernel(
 }
 
 // one CTA per output element; fp64, fixed order
-__global__ void __launch_bounds__(256) reduce_partials_kernel(const float* __restrict__ partials,
+__global__ void __launch_bounds__(256) reduce_partials_kernel(const float* partials,
                                                               int64_t num_parts, int np, int dd,
                                                               float* __restrict__ dA,
                                                               float* __restrict__ dB) {
   __shared__ double red[256];
   const int e = blockIdx.x;
   double s = 0.0;
-  for (int64_t p = threadIdx.x; p < num_parts; p += 256) s += partials[p * np + e];
+  griddep_wait();  // the partials come from the kernel just before this one (see ld_global_f32)
+  griddep_launch_dependents();
+  for (int64_t p = threadIdx.x; p < num_parts; p += 256) s += ld_global_f32(partials + p * np + e);
   red[threadIdx.x] = s;
   __syncthreads();
   for (int off = 128; off > 0; off >>= 1) {
@@ -497,9 +501,8 @@ cudaError_t launch_simt_backward_dw(const void* X, const void* dY, bool bf16, in
 cudaError_t launch_reduce_partials(const float* partials, int64_t num_parts, int d, float* dA,
                                    float* dB, cudaStream_t s, int* launches) {
   const int np = d * d + d;
-  reduce_partials_kernel<<<np, 256, 0, s>>>(partials, num_parts, np, d * d, dA, dB);
   ++*launches;
-  return cudaGetLastError();
+  return launch_pdl(reduce_partials_kernel, np, 256, 0, s, partials, num_parts, np, d * d, dA, dB);
 }
 
 }  // namespace lcvq

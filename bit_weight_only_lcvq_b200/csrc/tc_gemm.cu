@@ -48,7 +48,9 @@
 #include "codec.cuh"
 #include "common.cuh"
 #include "decode_mma.cuh"
+#include "gemv_common.cuh"
 #include "internal.h"
+#include "pdl.cuh"
 #include "sm100.cuh"
 
 namespace lcvq {
@@ -312,11 +314,6 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if constexpr (!is_alg(KIND) && KIND != kGram) {  // these never touch A, B
-    if (threadIdx.x < D * D) sAm[threadIdx.x] = p.Amat[threadIdx.x];
-    if (KIND != kDw && threadIdx.x >= 64 && threadIdx.x < 64 + D)
-      sAm[D * D + threadIdx.x - 64] = p.Bvec[threadIdx.x - 64];
-  }
   if (warp == 1) {
     tmem_alloc(tmem_holder, kTmemCols);
     tmem_relinquish();
@@ -324,6 +321,15 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&tmA);
     tma_prefetch_map(&tmB);
+  }
+  // Programmatic dependent launch: what is set up above overlaps the kernel before
+  // this one; nothing it may have written is read, or read by it written, earlier.
+  griddep_wait();
+  griddep_launch_dependents();
+  if constexpr (!is_alg(KIND) && KIND != kGram) {  // these never touch A, B
+    if (threadIdx.x < D * D) sAm[threadIdx.x] = p.Amat[threadIdx.x];
+    if (KIND != kDw && threadIdx.x >= 64 && threadIdx.x < 64 + D)
+      sAm[D * D + threadIdx.x - 64] = p.Bvec[threadIdx.x - 64];
   }
   tc_fence_before();
   __syncthreads();
@@ -655,11 +661,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if constexpr (KIND != kFwdAlg) {
-    if (threadIdx.x < D * D) sAm[threadIdx.x] = p.Amat[threadIdx.x];
-    if (KIND != kDw && threadIdx.x >= 64 && threadIdx.x < 64 + D)
-      sAm[D * D + threadIdx.x - 64] = p.Bvec[threadIdx.x - 64];
-  }
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, kTmemCols);
     tmem_relinquish_pair();
@@ -667,6 +668,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
   if (warp == 0 && lane == 0) {
     tma_prefetch_map(&tmA);
     tma_prefetch_map(&tmB);
+  }
+  // programmatic dependent launch: as tc_gemm_kernel
+  griddep_wait();
+  griddep_launch_dependents();
+  if constexpr (KIND != kFwdAlg) {
+    if (threadIdx.x < D * D) sAm[threadIdx.x] = p.Amat[threadIdx.x];
+    if (KIND != kDw && threadIdx.x >= 64 && threadIdx.x < 64 + D)
+      sAm[D * D + threadIdx.x - 64] = p.Bvec[threadIdx.x - 64];
   }
   tc_fence_before();
   __syncthreads();
@@ -1049,8 +1058,7 @@ cudaError_t launch_kind(const CUtensorMap& a, const CUtensorMap& b, const Params
   if (tiles < grid) grid = static_cast<int>(tiles);
   if (grid < 1) grid = 1;
   if (grid_out) *grid_out = grid;
-  kern<<<grid, C::kThreads, kSmemBytes, s>>>(a, b, p);
-  return cudaGetLastError();
+  return launch_pdl(kern, grid, C::kThreads, kSmemBytes, s, a, b, p);
 }
 
 template <int KIND, int DW>
@@ -1077,8 +1085,7 @@ cudaError_t launch_kind2(const CUtensorMap& a, const CUtensorMap& b, const Param
   if (tiles < pairs) pairs = static_cast<int>(tiles);
   if (pairs < 1) pairs = 1;
   if (grid_out) *grid_out = 2 * pairs;
-  kern<<<2 * pairs, C::kThreads, C::kSmem, s>>>(a, b, p);
-  return cudaGetLastError();
+  return launch_pdl(kern, 2 * pairs, C::kThreads, C::kSmem, s, a, b, p);
 }
 
 template <int KIND, int DW>
