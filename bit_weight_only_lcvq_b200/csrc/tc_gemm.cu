@@ -272,6 +272,28 @@ __device__ __forceinline__ void dw_block_partials(const Params& p, float (&pa)[D
   }
 }
 
+// The MMA issuer's role, run by the whole warp with an elected issuer (kWhole) or by
+// lane 0 alone.
+template <bool kWhole>
+__device__ __forceinline__ bool agree(bool ok) {
+  if constexpr (kWhole) return __all_sync(0xffffffffu, ok);
+  else return ok;
+}
+template <bool kWhole>
+__device__ __forceinline__ bool aborted(volatile int* flag) {
+  if constexpr (kWhole) return __shfl_sync(0xffffffffu, *flag, 0) != 0;
+  else return *flag != 0;
+}
+template <bool kWhole>
+__device__ __forceinline__ bool issuer() {
+  if constexpr (kWhole) return elect_one();
+  else return true;
+}
+template <bool kWhole>
+__device__ __forceinline__ void regroup() {
+  if constexpr (kWhole) __syncwarp();
+}
+
 template <int KIND, int D, int DW>
 __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -742,30 +764,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (rank == 0) {
+    // With decoders beside it lane 0 issues alone: a whole warp polling the decoders'
+    // barriers slows their handover (decode form at 2048 x 4096 -> 11008: 207 us
+    // against 243), more than its issue costs.
+    constexpr bool kWhole = !C::kHasCodes;
+    if (rank == 0 && (kWhole || lane == 0)) {
       constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, BN, C::kAmn, C::kBmn);
       int s = 0;
       uint32_t ph = 0;
       int64_t local = 0, it = 0;
       bool issued = false, ok = true;
-      for (int64_t tile = pair; tile < tiles && ok && !warp_abort(); tile += npairs, ++local) {
+      for (int64_t tile = pair; tile < tiles && ok && !aborted<kWhole>(abort_flag); tile += npairs, ++local) {
         const int buf = static_cast<int>(local & 1);
         const uint32_t use = static_cast<uint32_t>(local >> 1);
         // the odd CTA's epilogue arrives from the other SM: acquire at cluster scope
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[buf], (use & 1) ^ 1, lim))) {
+        if (!agree<kWhole>(mbar_wait_cluster(&tempty[buf], (use & 1) ^ 1, lim))) {
           fail(p, abort_flag, 12);
           break;
         }
         tc_fence_after();
         const uint32_t dt = tmem + buf * BN;
         for (int64_t kb = 0; kb < kblocks; ++kb, ++it) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&fullA[s], ph, lim))) {
+          if (!agree<kWhole>(mbar_wait(&fullA[s], ph, lim))) {
             fail(p, abort_flag, 13);
             ok = false;
             break;
           }
           if constexpr (C::kHasCodes) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&decd[s], ph, lim))) {
+            if (!agree<kWhole>(mbar_wait(&decd[s], ph, lim))) {
               fail(p, abort_flag, 14);
               ok = false;
               break;
@@ -773,7 +799,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
             // the odd CTA's half of B: one cluster-scope wait per group of k blocks
             const int64_t q = it / kPeerGroup;
             if (it % kPeerGroup == 0 &&
-                !__all_sync(0xffffffffu, mbar_wait_cluster(&decd_peer[q % S],
+                !agree<kWhole>(mbar_wait_cluster(&decd_peer[q % S],
                                                            static_cast<uint32_t>((q / S) & 1), lim))) {
               fail(p, abort_flag, 18);
               ok = false;
@@ -783,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
           tc_fence_after();
           const uint32_t a0 = smem_u32(smem + size_t(s) * C::kStage);
           const uint32_t b0 = a0 + C::kA;
-          if (elect_one()) {
+          if (issuer<kWhole>()) {
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
               const uint64_t ad = C::kAmn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
@@ -794,17 +820,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<KIND, DW>::kThr
             }
             mma_commit_pair(&empty[s]);
           }
-          __syncwarp();
+          regroup<kWhole>();
           issued = true;
           if (++s == S) { s = 0; ph ^= 1; }
         }
         if (!ok) break;
-        if (elect_one()) mma_commit_pair(&tfull[buf]);
-        __syncwarp();
+        if (issuer<kWhole>()) mma_commit_pair(&tfull[buf]);
+        regroup<kWhole>();
       }
       if (issued) {
-        if (elect_one()) mma_commit_pair(drain);
-        __syncwarp();
+        if (issuer<kWhole>()) mma_commit_pair(drain);
+        regroup<kWhole>();
         // the default limit: TMEM may be released only after the running MMAs
         if (!mbar_wait(drain, 0, kDefaultWaitLimit)) fail(p, abort_flag, 15);
       }
