@@ -2,8 +2,8 @@
 // writes X'' in the decoder's order (see xform.cu), the per-row constant of the
 // integer-code GEMM, and X packed into mx8 (see mx.cuh).
 //
-// The codes enter the GEMM as 128 + 2^b z, b = 3 at even positions and 5 at odd ones
-// (tc_gemm.cu kind FwdTop), so with X'r = bf16(X') and X''_k = X'r_k 2^-b
+// The codes enter the GEMM as 128 + 2^b z, b = 1, 3 or 5 by the position c of a word's
+// pair (b = 1 + 2 (c mod 3); tc_gemm.cu kind FwdTop), so with X'r = bf16(X') and X''_k = X'r_k 2^-b
 //     sum_k X''_k (128 + 2^b z_k) = sum_k X'r_k z_k + 128 sum_k X''_k,
 //     Y[m][n] = that + corr,  corr = s' - 3/2 sum_k X'r_k - 128 sum_k X''_k,
 // s' = sum_g x_g^T (B + 3/2 A 1): the centred algebraic form.
@@ -53,9 +53,15 @@ __device__ __forceinline__ float2 halves(uint64_t v) {
   return r;
 }
 
-// X'' of one 16-element block and its part of corr, on paired multiply-adds.  sAs is A
-// with its even columns / 8 and its odd ones / 32 (d = 1: A): powers of two, so
-// rounding commutes with them.
+// 2^-b of position k
+__device__ __forceinline__ float top_scale(int k) {
+  const int c = k & 7;
+  return c % 3 == 0 ? 0.5f : (c % 3 == 1 ? 0.125f : 0.03125f);
+}
+
+// X'' of one 16-element block and its part of corr, on paired multiply-adds.  d = 8:
+// sAs is A with column j times 2^-b(j); otherwise it is A, and X' is scaled after the
+// sums.  Powers of two, so rounding commutes with them.
 //   o[c] = bf16x2 of positions c and c + 8
 //   sb = sum x B';  off = 3/2 sum X'r + 128 sum X''
 template <int D>
@@ -66,7 +72,7 @@ __device__ __forceinline__ void top_block(const uint4& u0, const uint4& u1, cons
   float xp[16];
   if constexpr (D == 1) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) xp[k] = x(k) * (sAs[0] * (k & 1 ? 0.03125f : 0.125f));
+    for (int k = 0; k < 16; ++k) xp[k] = x(k) * sAs[0];
   } else {
     constexpr int kV = 16 / D, kJ = D / 2;  // vectors, pairs of columns
     uint64_t acc[kV][kJ] = {};
@@ -94,13 +100,14 @@ __device__ __forceinline__ void top_block(const uint4& u0, const uint4& u1, cons
   sb = 0.f;
 #pragma unroll
   for (int k = 0; k < 16; ++k) sb = fmaf(x(k), sBp[k % D], sb);
-  float part[2] = {0.f, 0.f};  // sums of X'' at even and odd positions
+  float part[3] = {0.f, 0.f, 0.f};  // sums of X'' by b
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    o[c] = pack_bf16x2(xp[c], xp[c + 8]);
-    part[c & 1] += bf16_lo(o[c]) + bf16_hi(o[c]);
+    const float s = D == 8 ? 1.f : top_scale(c);
+    o[c] = pack_bf16x2(xp[c] * s, xp[c + 8] * s);
+    part[c % 3] += bf16_lo(o[c]) + bf16_hi(o[c]);
   }
-  off = (1.5f * 8.f + 128.f) * part[0] + (1.5f * 32.f + 128.f) * part[1];
+  off = (1.5f * 2.f + 128.f) * part[0] + (1.5f * 8.f + 128.f) * part[1] + (1.5f * 32.f + 128.f) * part[2];
 }
 
 template <int D>
@@ -119,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   __syncthreads();
   if (threadIdx.x < D) sBp[threadIdx.x] = shifted_offset<D>(sA + threadIdx.x * D, sB[threadIdx.x]);
   __syncthreads();
-  if (D > 1 && threadIdx.x < D * D) sA[threadIdx.x] *= threadIdx.x & 1 ? 0.03125f : 0.125f;  // see top_block
+  if (D == 8 && threadIdx.x < D * D) sA[threadIdx.x] *= top_scale(threadIdx.x);  // see top_block
   __syncthreads();
 
   const int64_t blocks = d_in / 16, tiles_k = mx::scale_tiles_k(d_in);

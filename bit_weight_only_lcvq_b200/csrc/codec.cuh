@@ -60,16 +60,19 @@ __device__ __forceinline__ void dec_word(uint32_t w, uint4& c0, uint4& c1) {
   c1 = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Pairs (128 + 8 z_c, 128 + 8 z_{c+8}) for even c and (128 + 32 z_c, ..) for odd c, in
-// the same order: the codes of pairs 2 g and 2 g + 1 land in mantissa bits 3, 4 and 5, 6
-// by one shift.
+// Pairs (128 + 2^b z_c, 128 + 2^b z_{c+8}) with b = 1 + 2 (c mod 3), in the same order:
+// dec_word's codes one mantissa bit higher, for one shift more.
 __device__ __forceinline__ void dec_word_top(uint32_t w, uint4& c0, uint4& c1) {
-  const uint32_t src[4] = {w << 3, w >> 1, w >> 5, w >> 9};
+  const uint32_t src[3] = {w << 1, w >> 5, w >> 11};
   uint32_t o[8];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(o[2 * g]) : "r"(src[g]), "n"(0x00180018u), "n"(0x43004300u));
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(o[2 * g + 1]) : "r"(src[g]), "n"(0x00600060u), "n"(0x43004300u));
+  for (int c = 0; c < 8; ++c) {
+    if (c % 3 == 0)
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(o[c]) : "r"(src[c / 3]), "n"(0x00060006u), "n"(0x43004300u));
+    else if (c % 3 == 1)
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(o[c]) : "r"(src[c / 3]), "n"(0x00180018u), "n"(0x43004300u));
+    else
+      asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(o[c]) : "r"(src[c / 3]), "n"(0x00600060u), "n"(0x43004300u));
   }
   c0 = make_uint4(o[0], o[1], o[2], o[3]);
   c1 = make_uint4(o[4], o[5], o[6], o[7]);

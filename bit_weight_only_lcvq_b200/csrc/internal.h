@@ -45,8 +45,8 @@ cudaError_t launch_xform_i8(const uint16_t* X, int64_t M, int64_t d_in, int d, c
                             const float* B, uint8_t* X8, float* corr, float* inv_s, cudaStream_t s,
                             int* launches);
 
-// In one pass over X: X packed into mx8, X'' = bf16(X') / 8 and / 32 (even and odd
-// positions) in the decoder's order, and corr[M] = s' - 3/2 sum bf16(X') - 128 sum X''
+// In one pass over X: X packed into mx8, X'' = bf16(X') 4^-p / 2 in the decoder's
+// order, and corr[M] = s' - 3/2 sum bf16(X') - 128 sum X''
 cudaError_t launch_xform_ckpt(const uint16_t* X, int64_t M, int64_t d_in, int d, const float* A,
                               const float* B, uint16_t* Xpp, float* corr, uint8_t* X8, uint8_t* S8,
                               cudaStream_t s, int* launches);
@@ -157,7 +157,7 @@ cudaError_t launch_tc_forward(const uint16_t* Xa, bool algebraic, const float* c
                               const uint8_t* packed, int64_t d_out, int64_t d_in, int d,
                               const float* A, const float* B, uint16_t* Y, unsigned int* err,
                               cudaStream_t s, int* launches);
-// the algebraic form with codes as 128 + 8 z and 128 + 32 z, on X'' and corr of launch_xform_ckpt
+// the algebraic form with codes as 128 + 2 4^p z, on X'' and corr of launch_xform_ckpt
 cudaError_t launch_tc_forward_top(const uint16_t* Xpp, const float* corr, int64_t M,
                                   const uint8_t* packed, int64_t d_out, int64_t d_in, uint16_t* Y,
                                   unsigned int* err, cudaStream_t s, int* launches);

@@ -18,14 +18,14 @@
 //   FwdAlg  Y[m][n]  = sum_k X''[m][k] v[n][k] + corr[m]      A = X'' (K-major)
 //           v = 128 + 4^p z: one LOP3 per bf16 pair (see xform.cu)
 //   FwdTop  Y[m][n]  = sum_k X''[m][k] v[n][k] + corr[m]      A = X'' (K-major)
-//           v = 128 + 8 z and 128 + 32 z at even and odd positions (codec.cuh,
-//           dec_word_top; two instructions more per 16 codes), X'' = bf16(X') / 8 and
-//           / 32.  Offsets of 16 and 4 beside z keep the fp32 sums small; with
-//           FwdAlg's 128, 32 and 8 they run 60 times as high as Y, and over a long K
-//           the additions, which the tensor core truncates, show in Y (8192 x 14336
-//           -> 4096: 2.6e-3 of its norm against 2.35e-3, which X' and Y rounded to
-//           bf16 make).  Cleaner decoders cost more, since the power limit paces
-//           this kernel: every code in the top bits 777 us, 128 subtracted 795
+//           v = 128 + 2 4^p z: FwdAlg's codes one mantissa bit higher (codec.cuh,
+//           dec_word_top; one instruction more per 16 codes), X'' = bf16(X') 4^-p / 2.
+//           The offsets beside z are 64, 16 and 4 instead of 128, 32 and 8, so the fp32
+//           sums run half as high; over a long K the additions, which the tensor core
+//           truncates, then no longer show in Y (8192 x 14336 -> 4096: 2.36e-3 of its
+//           norm, FwdAlg 2.6e-3; X' and Y rounded to bf16 make 2.35e-3).  It costs
+//           nothing (739 us, FwdAlg 744, measured in turn); every code in the top bits
+//           or 128 subtracted took 2 and 4% more for 2.34e-3
 //   FwdDec  Y[m][n]  = sum_k X[m][k] bf16(A z + B)[n][k]      A = X (K-major)
 //           decoders evaluate A z + B in fp32 (LC-QAT Methodology 1, c = A z + B)
 //   Dx      P[m][k]  = sum_n dY[m][n] v[n][k]                 A = dY (K-major),
