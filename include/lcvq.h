@@ -444,7 +444,8 @@ LCVQ_API lcvq_status lcvq_mx4_gemm(const uint8_t* X4, const uint8_t* SX, int64_t
  * MX8 exactly as lcvq_mx_pack packs it (ld = d_in), for lcvq_gemm_backward_ckpt.
  * For bf16 and M > 32 one pass over X forms bf16(X') and packs X, and the codes
  * enter the GEMM as 128 + 2 4^p z instead of 128 + 4^p z: Y is the algebraic form's
- * to within the rounding of its fp32 sums (smaller here), not bit for bit.  Otherwise Y has lcvq_gemm's bits (form AUTO).
+ * to within the rounding of its fp32 sums (smaller here), not bit for bit.
+ * Otherwise Y has lcvq_gemm's bits (form AUTO).
  *   X8 [M][d_in] and S8 (lcvq_mx_scale_bytes(M, d_in) bytes) out; the rest as
  *   lcvq_gemm.
  *   workspace: >= lcvq_workspace_size(LCVQ_OP_GEMM_CKPT, dtype, M, d_out, d_in, d)
