@@ -112,6 +112,12 @@ BwdWs bwd_ws(int64_t M, int64_t d_out, int64_t d_in, int d) {
   return w;
 }
 
+// forward that keeps X: the plain forward's scratch, then the parts of a split K
+size_t ckpt_ws(lcvq_dtype dtype, int64_t M, int64_t d_out, int64_t d_in) {
+  const size_t total = gemm_ws(dtype, M, d_in).total;
+  if (dtype != LCVQ_BF16 || M <= 32 || d_out == 0 || d_in == 0) return total;
+  return round_up(total + tc_top_parts_bytes(M, d_out, d_in), 256);
+}
 // backward from a kept X: the plain backward's scratch, then the values of X
 size_t bwd_ckpt_values_off(int64_t M, int64_t d_out, int64_t d_in, int d) {
   return round_up(bwd_ws(M, d_out, d_in, d).total, 256);
@@ -192,7 +198,7 @@ size_t lcvq_workspace_size(lcvq_op op, lcvq_dtype dtype, int64_t M, int64_t d_ou
   if (op == LCVQ_OP_ASSIGN_LDLQ) return kWsHeaderBytes + ldlq_workspace_bytes(d_out, d_in);
   if (op == LCVQ_OP_FIT_AFFINE_H) return kWsHeaderBytes + fith_scratch_bytes(d_out, d_in, d);
   if (op == LCVQ_OP_MX4_GEMM) return kWsHeaderBytes;
-  if (op == LCVQ_OP_GEMM_CKPT) return gemm_ws(dtype, M, d_in).total;
+  if (op == LCVQ_OP_GEMM_CKPT) return ckpt_ws(dtype, M, d_out, d_in);
   if (op == LCVQ_OP_GEMM_BACKWARD_CKPT) return bwd_ckpt_ws(dtype, M, d_out, d_in, d);
   return 0;
 }
@@ -631,7 +637,7 @@ lcvq_status lcvq_gemm_ckpt(const void* X, lcvq_dtype dtype, int64_t M, const uin
       if (!Y || !packed || !A || !B || !workspace) return LCVQ_ERR_INVALID_ARG;
       if (!aligned16(Y) || !aligned16(packed) || !aligned16(A) || !aligned16(B) || !aligned256(workspace))
         return LCVQ_ERR_ALIGNMENT;
-      if (ws_bytes < gemm_ws(dtype, M, d_in).total) return LCVQ_ERR_WORKSPACE;
+      if (ws_bytes < ckpt_ws(dtype, M, d_out, d_in)) return LCVQ_ERR_WORKSPACE;
     }
     if (lcvq_status st = check_device(); st != LCVQ_OK) return st;
   }
@@ -647,6 +653,7 @@ lcvq_status lcvq_gemm_ckpt(const void* X, lcvq_dtype dtype, int64_t M, const uin
                                       S8, s, &launches);
     if (e == cudaSuccess)
       e = launch_tc_forward_top(Xpp, corr, M, packed, d_out, d_in, static_cast<uint16_t*>(Y),
+                                reinterpret_cast<float*>(ws + w.total),
                                 reinterpret_cast<unsigned int*>(ws), s, &launches);
     return finish(e, launches);
   }

@@ -158,9 +158,14 @@ cudaError_t launch_tc_forward(const uint16_t* Xa, bool algebraic, const float* c
                               const float* A, const float* B, uint16_t* Y, unsigned int* err,
                               cudaStream_t s, int* launches);
 // the algebraic form with codes as 128 + 2 4^p z, on X'' and corr of launch_xform_ckpt
+// (few tiles and a long K: in tc_top_splits() > 1 parts of K, parts: their [M][d_out]
+// fp32 sums, joined by a second launch)
+int tc_top_splits(int64_t M, int64_t d_out, int64_t d_in);
+// bytes of `parts` that serve every batch of at most M rows
+size_t tc_top_parts_bytes(int64_t M, int64_t d_out, int64_t d_in);
 cudaError_t launch_tc_forward_top(const uint16_t* Xpp, const float* corr, int64_t M,
                                   const uint8_t* packed, int64_t d_out, int64_t d_in, uint16_t* Y,
-                                  unsigned int* err, cudaStream_t s, int* launches);
+                                  float* parts, unsigned int* err, cudaStream_t s, int* launches);
 cudaError_t launch_tc_backward_dx(const uint16_t* dY, const float* rsum, int64_t M,
                                   const uint8_t* packed, int64_t d_out, int64_t d_in, int d,
                                   const float* A, const float* B, uint16_t* dX, unsigned int* err,

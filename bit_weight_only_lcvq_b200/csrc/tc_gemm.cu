@@ -71,8 +71,9 @@ constexpr int C_BYTES = 4096;         // packed codes of one stage
 constexpr int kPairPeerGroup = 3;
 constexpr int kTmemCols = 512;
 
-enum Kind { kFwdAlg = 0, kFwdDec = 1, kDx = 2, kDw = 3, kGram = 4, kFwdTop = 5 };
-constexpr bool is_alg(int kind) { return kind == kFwdAlg || kind == kFwdTop; }
+enum Kind { kFwdAlg = 0, kFwdDec = 1, kDx = 2, kDw = 3, kGram = 4, kFwdTop = 5, kFwdTopParts = 6 };
+constexpr bool is_top(int kind) { return kind == kFwdTop || kind == kFwdTopParts; }
+constexpr bool is_alg(int kind) { return kind == kFwdAlg || is_top(kind); }
 
 struct Params {
   int64_t M, N, K;    // D is M x N, contraction K (see each kind)
@@ -86,6 +87,7 @@ struct Params {
   void* out;
   float* partials;
   unsigned int* err;
+  int splits;  // FwdTopParts: parts of K, each with its own fp32 D in `partials` ([split][M][N])
 };
 
 template <int KIND, int DW>
@@ -321,6 +323,23 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
   const int64_t m_tiles = ceil_div(p.M, BM), n_tiles = ceil_div(p.N, BN);
   const int64_t tiles = m_tiles * n_tiles;
   const int64_t kblocks = ceil_div(p.K, BK);
+  // FwdTopParts: the CTAs take (tile, part of K) units in turn, at most one unit an SM, so
+  // units and k blocks x parts fit 32 bits.  A kind of its own: the unit arithmetic
+  // would cost an unsplit FwdTop call 1% (75.3 -> 76.1 us at 2048 x 4096 -> 4096).
+  constexpr bool kParts = KIND == kFwdTopParts;
+  const uint32_t parts = kParts ? static_cast<uint32_t>(p.splits) : 1;
+  const int64_t units = tiles * parts;
+  auto tile_of = [&](int64_t unit) -> int64_t {
+    if constexpr (kParts) return static_cast<uint32_t>(unit) / parts;
+    else return unit;
+  };
+  auto part_kb = [&](int64_t unit, uint32_t next) -> int64_t {  // first k block of the unit's part (+ next)
+    if constexpr (kParts)
+      return static_cast<uint32_t>(kblocks) * (static_cast<uint32_t>(unit) % parts + next) / parts;
+    else return next ? kblocks : 0;
+  };
+  auto first_kb = [&](int64_t unit) { return part_kb(unit, 0); };
+  auto end_kb = [&](int64_t unit) { return part_kb(unit, 1); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -369,10 +388,10 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
     uint32_t ph = 0;
     int64_t issued = 0;
     bool ok = true;
-    for (int64_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+    for (int64_t unit = blockIdx.x; unit < units && ok; unit += gridDim.x) {
       int mt, nt;
-      tile_coords(tile, m_tiles, n_tiles, kBand, mt, nt);
-      for (int64_t kb = 0; kb < kblocks; ++kb) {
+      tile_coords(tile_of(unit), m_tiles, n_tiles, kBand, mt, nt);
+      for (int64_t kb = first_kb(unit), kb_end = end_kb(unit); kb < kb_end; ++kb) {
         if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1, lim))) {
           fail(p, abort_flag, 1);
           ok = false;
@@ -412,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
     uint32_t ph = 0;
     int64_t local = 0;
     bool issued = false, ok = true;
-    for (int64_t tile = blockIdx.x; tile < tiles && ok && !warp_abort(); tile += gridDim.x, ++local) {
+    for (int64_t unit = blockIdx.x; unit < units && ok && !warp_abort(); unit += gridDim.x, ++local) {
       const int buf = static_cast<int>(local & 1);
       const uint32_t use = static_cast<uint32_t>(local >> 1);
       if (!__all_sync(0xffffffffu, mbar_wait(&tempty[buf], (use & 1) ^ 1, lim))) {
@@ -421,7 +440,8 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
       }
       tc_fence_after();
       const uint32_t dt = tmem + buf * BN;
-      for (int64_t kb = 0; kb < kblocks; ++kb) {
+      const int64_t kb_first = first_kb(unit), kb_end = end_kb(unit);
+      for (int64_t kb = kb_first; kb < kb_end; ++kb) {
         uint64_t* ready = (DW > 0) ? &decd[s] : &full[s];
         if (!__all_sync(0xffffffffu, mbar_wait(ready, ph, lim))) {
           fail(p, abort_flag, 3);
@@ -438,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
                                         : sdesc_sw128(a0 + k * 32, 16, 1024);
             const uint64_t bd = C::kBmn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
                                         : sdesc_sw128(b0 + k * 32, 16, 1024);
-            mma_ss(dt, ad, bd, idesc, (kb | k) != 0 ? 1u : 0u);
+            mma_ss(dt, ad, bd, idesc, kb != kb_first || k != 0 ? 1u : 0u);
           }
           mma_commit(&empty[s]);
         }
@@ -464,8 +484,8 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
     const int dt = (threadIdx.x - 64) % (32 * GW);
     int s = 0, turn = 0;  // turn: the group that owns the next k block
     uint32_t ph = 0;
-    for (int64_t tile = blockIdx.x; tile < tiles && !warp_abort(); tile += gridDim.x) {
-      for (int64_t kb = 0; kb < kblocks; ++kb) {
+    for (int64_t unit = blockIdx.x; unit < units && !warp_abort(); unit += gridDim.x) {
+      for (int64_t kb = first_kb(unit), kb_end = end_kb(unit); kb < kb_end; ++kb) {
         const bool mine = turn == grp;
         if (++turn == C::kDecGroups) turn = 0;
         if (!mine) {
@@ -488,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint4 c0, c1;
-              if constexpr (KIND == kFwdTop) dec_word_top(w[q], c0, c1);
+              if constexpr (is_top(KIND)) dec_word_top(w[q], c0, c1);
               else dec_word(w[q], c0, c1);
               st_shared_v4(row + (((2 * q) ^ (r & 7)) << 4), c0);
               st_shared_v4(row + (((2 * q + 1) ^ (r & 7)) << 4), c1);
@@ -562,9 +582,9 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
       for (int i = 0; i < D; ++i) pb[i] = 0.f;
     }
     int64_t local = 0;
-    for (int64_t tile = blockIdx.x; tile < tiles && !warp_abort(); tile += gridDim.x, ++local) {
+    for (int64_t unit = blockIdx.x; unit < units && !warp_abort(); unit += gridDim.x, ++local) {
       int mt, nt;
-      tile_coords(tile, m_tiles, n_tiles, kBand, mt, nt);
+      tile_coords(tile_of(unit), m_tiles, n_tiles, kBand, mt, nt);
       const int buf = static_cast<int>(local & 1);
       const uint32_t use = static_cast<uint32_t>(local >> 1);
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[buf], use & 1, lim))) {  // one outcome per warp
@@ -585,6 +605,16 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
         tmem_ld_wait();
         const int64_t gn0 = int64_t(nt) * BN + c * 32;  // first D column of the chunk
         if (gm >= p.M || gn0 >= p.N) continue;
+        if constexpr (kParts) {  // this part's sums; top_join_kernel adds them up
+          float* o = p.partials + (int64_t(static_cast<uint32_t>(unit) % parts) * p.M + gm) * p.N + gn0;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (gn0 + 4 * q < p.N)
+              reinterpret_cast<float4*>(o)[q] =
+                  make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                              __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+          continue;
+        }
         DwBits bits{};
         if constexpr (KIND == kDw) bits = dw_bits(p, gm, gn0);
         epilogue_chunk<KIND, D>(p, sAm, r, gm, gn0, addc, rs, pa, pb, bits);
@@ -602,6 +632,26 @@ __global__ void __launch_bounds__(Cfg<KIND, DW>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Y[m][n] = sum over the parts of K, in order, + corr[m]; eight columns a thread
+__global__ void __launch_bounds__(256) top_join_kernel(const float* part, int splits, int64_t M, int64_t N,
+                                                       const float* corr, uint16_t* __restrict__ Y) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (e >= M * N) return;
+  const float c = ld_global_f32(corr + e / N);
+  float s[8] = {};
+  for (int p = 0; p < splits; ++p) {
+    const uint4 u = ld_global_v4(part + p * M * N + e), v = ld_global_v4(part + p * M * N + e + 4);
+    const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] += __uint_as_float(w[i]);
+  }
+  *reinterpret_cast<uint4*>(Y + e) =
+      make_uint4(pack_bf16x2(s[0] + c, s[1] + c), pack_bf16x2(s[2] + c, s[3] + c),
+                 pack_bf16x2(s[4] + c, s[5] + c), pack_bf16x2(s[6] + c, s[7] + c));
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -1079,7 +1129,7 @@ cudaError_t launch_kind(const CUtensorMap& a, const CUtensorMap& b, const Params
   if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kSmemBytes);
       e != cudaSuccess)
     return e;
-  const int64_t tiles = ceil_div(p.M, BM) * ceil_div(p.N, BN);
+  const int64_t tiles = ceil_div(p.M, BM) * ceil_div(p.N, BN) * (KIND == kFwdTopParts ? p.splits : 1);
   int grid = num_sms();
   if (tiles < grid) grid = static_cast<int>(tiles);
   if (grid < 1) grid = 1;
@@ -1156,9 +1206,35 @@ cudaError_t launch_tc_forward(const uint16_t* Xa, bool algebraic, const float* c
   return e;
 }
 
+int tc_top_splits(int64_t M, int64_t d_out, int64_t d_in) {
+  // Few tiles and a long K: one CTA's chain of k blocks sets the time (0.44 us each).
+  // Parts of at least 16 k blocks, up to eight and as many as the SMs have room for:
+  // a whole call, us, one part -> split: 64 x 4096 -> 4096 35.0 -> 16.8 (4 parts);
+  // 512 x 4096 -> 4096 37.6 -> 31.4 (2); 64 x 11008 -> 4096 82.6 -> 23.0 (8);
+  // 512 x 11008 -> 4096 87.5 -> 59.3 (2); 128 x 2048 -> 4096 21.1 -> 19.7 (2, the least gain).
+  // k blocks times parts stay within 32 bits, as d_in does.
+  const int64_t tiles = ceil_div(M, BM) * ceil_div(d_out, BN), kb = ceil_div(d_in, BK);
+  int64_t n = kNumSMsB200 / tiles;
+  if (n > kb / 16) n = kb / 16;
+  return n < 2 ? 1 : static_cast<int>(n > 8 ? 8 : n);
+}
+
+size_t tc_top_parts_bytes(int64_t M, int64_t d_out, int64_t d_in) {
+  // fewer rows can take more parts: for each count, the most rows that take it
+  const int64_t n_tiles = ceil_div(d_out, BN), kb = ceil_div(d_in, BK);
+  size_t most = 0;
+  for (int n = 2; n <= 8 && n <= kb / 16; ++n) {
+    int64_t rows = kNumSMsB200 / (n * n_tiles) * BM;
+    if (rows > M) rows = M;
+    const size_t bytes = size_t(n) * size_t(rows) * size_t(d_out) * 4;
+    if (bytes > most) most = bytes;
+  }
+  return most;
+}
+
 cudaError_t launch_tc_forward_top(const uint16_t* Xpp, const float* corr, int64_t M,
                                   const uint8_t* packed, int64_t d_out, int64_t d_in, uint16_t* Y,
-                                  unsigned int* err, cudaStream_t s, int* launches) {
+                                  float* parts, unsigned int* err, cudaStream_t s, int* launches) {
   CUtensorMap ta, tb;
   if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Xpp, d_in, M, d_in * 2, BK, BM, true) ||
       !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, packed, d_in / 4, d_out, d_in / 4, BK / 4, BN, false))
@@ -1166,9 +1242,15 @@ cudaError_t launch_tc_forward_top(const uint16_t* Xpp, const float* corr, int64_
   Params p{};
   p.M = M; p.N = d_out; p.K = d_in; p.d_in = d_in; p.d_out = d_out;
   p.codes = packed; p.corr = corr; p.out = Y; p.err = err;
-  cudaError_t e = launch_kind<kFwdTop, 8, kAlgDecWarps>(ta, tb, p, s, nullptr);
+  p.splits = tc_top_splits(M, d_out, d_in);
+  p.partials = parts;
+  cudaError_t e = p.splits == 1 ? launch_kind<kFwdTop, 8, kAlgDecWarps>(ta, tb, p, s, nullptr)
+                                : launch_kind<kFwdTopParts, 8, kAlgDecWarps>(ta, tb, p, s, nullptr);
   ++*launches;
-  return e;
+  if (e != cudaSuccess || p.splits == 1) return e;
+  ++*launches;
+  return launch_pdl(top_join_kernel, ceil_div(M * d_out, 8 * 256), 256, 0, s, parts, p.splits, M, d_out,
+                    corr, Y);
 }
 
 cudaError_t launch_tc_backward_dx(const uint16_t* dY, const float* rsum, int64_t M,

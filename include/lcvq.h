@@ -445,6 +445,8 @@ LCVQ_API lcvq_status lcvq_mx4_gemm(const uint8_t* X4, const uint8_t* SX, int64_t
  * For bf16 and M > 32 one pass over X forms bf16(X') and packs X, and the codes
  * enter the GEMM as 128 + 2 4^p z instead of 128 + 4^p z: Y is the algebraic form's
  * to within the rounding of its fp32 sums (smaller here), not bit for bit.
+ * Few output tiles and a long d_in are summed in two to eight parts of d_in, in
+ * fp32 in the workspace, added in order: the bits do not change from run to run.
  * Otherwise Y has lcvq_gemm's bits (form AUTO).
  *   X8 [M][d_in] and S8 (lcvq_mx_scale_bytes(M, d_in) bytes) out; the rest as
  *   lcvq_gemm.
@@ -475,7 +477,8 @@ LCVQ_API lcvq_status lcvq_gemm_backward_ckpt(const uint8_t* X8, const uint8_t* S
 /* Workspace bytes a call with these arguments needs (0 on invalid input).
  * The workspace holds the device error word (its first 256 bytes, which the
  * caller zeroes once before first use), the transformed activations of the
- * algebraic form and the per-block partial sums of dA/dB.  A workspace may be
+ * algebraic form, the per-block partial sums of dA/dB and the fp32 parts of a
+ * split d_in (LCVQ_OP_GEMM_CKPT: enough for every smaller M too).  A workspace may be
  * reused by calls that are ordered on one stream; calls that may overlap on the
  * GPU need separate workspaces. */
 LCVQ_API size_t lcvq_workspace_size(lcvq_op op, lcvq_dtype dtype, int64_t M, int64_t d_out,

@@ -299,7 +299,8 @@ def layer(seed, M, K, N, d, dtype):
 
 CKPT = [(1, 64, 8, 8, BF16), (16, 512, 512, 4, F32), (3, 192, 136, 1, BF16), (16, 512, 512, 8, BF16),
         (33, 448, 200, 2, BF16), (77, 192, 72, 2, F32), (130, 1088, 520, 4, BF16), (333, 1088, 520, 8, BF16),
-        (700, 576, 264, 1, BF16), (64, 320, 264, 8, F32)]
+        (700, 576, 264, 1, BF16), (64, 320, 264, 8, F32), (40, 4160, 72, 8, BF16), (330, 8320, 280, 4, BF16),
+        (130, 2112, 264, 2, BF16)]
 
 
 @pytest.mark.parametrize("M,K,N,d,dtype", CKPT)
@@ -325,6 +326,24 @@ def test_forward_keeps_x(M, K, N, d, dtype):
     want, byte = MX.pack(x, "mx8")
     assert np.array_equal(q.cpu().numpy(), want)
     assert np.array_equal(MX.untile_scales(s.cpu().numpy(), M, K), byte)
+
+
+def test_forward_keeps_x_one_workspace_for_all_batches():
+    """A workspace of exactly the size for the largest batch, its scratch full of
+    NaN bytes, gives every smaller batch (other splits of K) the bits of a fresh one."""
+    Wp, A, B, x, _ = layer(5, 400, 8320, 280, 4, BF16)
+    packed, _ = lcvq.assign_pack(to_dev(Wp, F32), 4)
+    X, At, Bt = to_dev(x, BF16), to_dev(A, F32), to_dev(B, F32)
+    n = lcvq.workspace_size(lcvq.OP_GEMM_CKPT, BF16, 400, 280, 8320, 4)
+    ws, buf = guarded((n,), torch.uint8)
+    ws[:256] = 0
+    ws[256:] = 0xFF
+    for M in (400, 40, 256, 130, 33, 5):
+        Y, _ = lcvq.gemm_ckpt(X[:M], packed, 8320, At, Bt, 4, workspace=ws)
+        want, _ = lcvq.gemm_ckpt(X[:M], packed, 8320, At, Bt, 4)
+        assert torch.equal(Y, want)
+    assert guard_intact(ws, buf)
+    assert lcvq.check_device_error(ws) == 0
 
 
 def grad_tolerance(dtype, M, terms):

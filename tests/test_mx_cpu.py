@@ -123,6 +123,14 @@ def test_mx4_gemm_refusals():
     assert call(M=0) == 0 and call(n=0) == 0
 
 
+@pytest.mark.parametrize("d_out,d_in", [(72, 4160), (264, 2112), (11008, 4096), (4096, 11008), (520, 1088)])
+def test_ckpt_workspace_serves_smaller_batches(d_out, d_in):
+    # what the largest batch asks for is enough for every smaller one
+    sizes = [lcvq.workspace_size(lcvq.OP_GEMM_CKPT, torch.bfloat16, M, d_out, d_in, 8)
+             for M in (0, 1, 16, 32, 33, 40, 127, 128, 129, 256, 300, 640, 1024, 2048, 8192, 20000)]
+    assert sizes == sorted(sizes)
+
+
 def test_ckpt_refusals():
     L = lcvq.lib()
     need = L.lcvq_workspace_size(lcvq.OP_GEMM_CKPT, 1, 4, 64, 64, 8)
